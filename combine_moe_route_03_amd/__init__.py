@@ -9,7 +9,9 @@ without it raises, there is no fallback.
 Entry points mirror include/moe_route.h: ``route``, ``dispatch_index``,
 ``route_index``, ``dispatch_copy``, ``dispatch``, ``dispatch_capacity``,
 ``expert_scale``, ``expert_scale_rows``, ``expert_swiglu``, ``combine``,
-``combine_rows``, ``stats``.
+``combine_rows``, ``stats``, and the 8-bit experts and the small layer:
+``quantize``, ``dispatch_copy_fp8``, ``expert_gemm_fp8``, ``expert_swiglu_fp8``,
+``layer``.
 """
 from __future__ import annotations
 
@@ -24,7 +26,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # build the CPU sanitizer run loads); there is no fallback when it is missing.
 LIB_PATH = os.environ.get("MOE_ROUTE_LIB") or os.path.join(_HERE, "libmoe_route.so")
 
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_F8E4M3 = 0, 1, 2
 _DTYPE_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _CODE_DTYPE = {v: k for k, v in _DTYPE_CODE.items()}
 
@@ -94,6 +96,16 @@ SIGNATURES = {
     "moe_expert_swiglu_workspace_bytes": ([_shp, _i32], ctypes.c_size_t),
     "moe_expert_swiglu": ([_shp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp,
                            _vp, _vp, _vp], ctypes.c_int),
+    "moe_quantize": ([_vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp], ctypes.c_int),
+    "moe_dispatch_copy_fp8": ([_shp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "moe_expert_gemm_fp8": ([_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+                            ctypes.c_int),
+    "moe_expert_swiglu_fp8_workspace_bytes": ([_shp, _i32], ctypes.c_size_t),
+    "moe_expert_swiglu_fp8": ([_shp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               ctypes.c_size_t, _vp], ctypes.c_int),
+    "moe_layer_workspace_bytes": ([_shp, _i32], ctypes.c_size_t),
+    "moe_layer": ([_shp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                   ctypes.c_size_t, _vp], ctypes.c_int),
     "moe_combine": ([_shp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
     "moe_stats": ([_vp, _i32, _i32, _vp, _vp], ctypes.c_int),
     "moe_dirichlet_alpha": ([_vp, _i32, _vp, _vp], ctypes.c_int),
@@ -639,6 +651,176 @@ def combine(expert_out: torch.Tensor, topk_w: torch.Tensor, pos: torch.Tensor, s
     _check(lib().moe_combine(ctypes.byref(sh), _ptr(expert_out), _ptr(topk_w), _ptr(pos), _ptr(y),
                              _stream()), "moe_combine")
     return y
+
+
+# ------------------------------------------------- 8-bit experts, small layer
+
+_FP8 = torch.float8_e4m3fn
+
+
+def _checked(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> int:
+    """Address of a contiguous tensor of this shape and type on the current device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmoe_route must be contiguous")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device, got {t.device}")
+    return t.data_ptr()
+
+
+def _current_stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def quantize(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None = None,
+             scale: torch.Tensor | None = None):
+    """Block quantisation of x [..., rows, cols] (float32 or bfloat16): (q
+    float8_e4m3fn of x's shape, scale float32 [..., ceil(rows/block_rows),
+    ceil(cols/128)]); block_rows 1 (tokens) or 128 (weights)."""
+    if x.dtype not in _DTYPE_CODE:
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() < 2 or block_rows not in (1, 128):
+        raise ValueError("x needs at least two dimensions, block_rows must be 1 or 128")
+    shape = tuple(x.shape)
+    lead, rows, cols = shape[:-2], shape[-2], shape[-1]
+    batch = 1
+    for n in lead:
+        batch *= n
+    sshape = (*lead, -(-rows // block_rows), _blocks(cols))
+    q = _empty(shape, _FP8, x.device) if q is None else q
+    scale = _empty(sshape, torch.float32, x.device) if scale is None else scale
+    _check(lib().moe_quantize(
+        _checked("x", x, shape, x.dtype), _DTYPE_CODE[x.dtype], batch, rows, cols, block_rows,
+        _checked("q", q, shape, _FP8), _checked("scale", scale, sshape, torch.float32),
+        _current_stream()), "moe_quantize")
+    return q, scale
+
+
+def dispatch_copy_fp8(x: torch.Tensor, pos: torch.Tensor, shape: Shape,
+                      send_q: torch.Tensor | None = None,
+                      send_scale: torch.Tensor | None = None):
+    """The dispatch copy with the rows quantised on the way: (send_q
+    float8_e4m3fn [T*k, H], send_scale float32 [T*k, ceil(H/128)])."""
+    T, H, k = shape.T, shape.H, shape.k
+    qs, ss = (T * k, H), (T * k, _blocks(H))
+    send_q = _empty(qs, _FP8, x.device) if send_q is None else send_q
+    send_scale = _empty(ss, torch.float32, x.device) if send_scale is None else send_scale
+    _check(lib().moe_dispatch_copy_fp8(
+        ctypes.byref(shape.c()), _checked("x", x, (T, H), shape.dtype),
+        _checked("pos", pos, (T, k), torch.int32), _checked("send_q", send_q, qs, _FP8),
+        _checked("send_scale", send_scale, ss, torch.float32), _current_stream()),
+        "moe_dispatch_copy_fp8")
+    return send_q, send_scale
+
+
+def expert_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: torch.Tensor,
+                    expert_counts: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Each expert's rows of a [rows, K] times its w [E, N, K], both float8_e4m3fn
+    with block scales, into bfloat16 [rows, N]."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, K] and w [E, N, K]")
+    rows, K = a.shape
+    E, N, _ = w.shape
+    out = _empty((rows, N), torch.bfloat16, a.device) if out is None else out
+    f32, i32 = torch.float32, torch.int32
+    _check(lib().moe_expert_gemm_fp8(
+        rows, E, N, K, _checked("a", a, (rows, K), _FP8),
+        _checked("a_scale", a_scale, (rows, _blocks(K)), f32),
+        _checked("expert_offsets", expert_offsets, (E,), i32),
+        _checked("expert_counts", expert_counts, (E,), i32), _checked("w", w, (E, N, K), _FP8),
+        _checked("w_scale", w_scale, (E, _blocks(N), _blocks(K)), f32),
+        _checked("out", out, (rows, N), torch.bfloat16), _current_stream()),
+        "moe_expert_gemm_fp8")
+    return out
+
+
+def expert_swiglu_fp8_workspace_bytes(shape: Shape, I: int) -> int:
+    return int(lib().moe_expert_swiglu_fp8_workspace_bytes(ctypes.byref(shape.c()), I))
+
+
+def _workspace(workspace: torch.Tensor | None, nbytes: int, device) -> torch.Tensor:
+    if workspace is None:
+        return _empty((max(nbytes, 1),), torch.uint8, device)
+    return workspace
+
+
+def expert_swiglu_fp8(send_q: torch.Tensor, send_scale: torch.Tensor,
+                      expert_offsets: torch.Tensor, expert_counts: torch.Tensor, shape: Shape,
+                      w_gate_up: torch.Tensor, s_gate_up: torch.Tensor, w_down: torch.Tensor,
+                      s_down: torch.Tensor, expert_out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """SwiGLU expert FFN on 8-bit rows and weights (w_gate_up [E, 2I, H], w_down
+    [E, H, I] float8_e4m3fn with 128 x 128 block scales) into bfloat16 [T*k, H].
+    shape.dtype is the output's: bfloat16."""
+    E, H, rows = shape.E, shape.H, shape.T * shape.k
+    I = w_down.shape[-1]
+    f32, i32 = torch.float32, torch.int32
+    expert_out = _empty((rows, H), torch.bfloat16, send_q.device) if expert_out is None \
+        else expert_out
+    workspace = _workspace(workspace, expert_swiglu_fp8_workspace_bytes(shape, I), send_q.device)
+    _check(lib().moe_expert_swiglu_fp8(
+        ctypes.byref(shape.c()), I, _checked("send_q", send_q, (rows, H), _FP8),
+        _checked("send_scale", send_scale, (rows, _blocks(H)), f32),
+        _checked("expert_offsets", expert_offsets, (E,), i32),
+        _checked("expert_counts", expert_counts, (E,), i32),
+        _checked("w_gate_up", w_gate_up, (E, 2 * I, H), _FP8),
+        _checked("s_gate_up", s_gate_up, (E, _blocks(2 * I), _blocks(H)), f32),
+        _checked("w_down", w_down, (E, H, I), _FP8),
+        _checked("s_down", s_down, (E, _blocks(H), _blocks(I)), f32),
+        _checked("expert_out", expert_out, (rows, H), torch.bfloat16),
+        _checked("workspace", workspace, tuple(workspace.shape), torch.uint8), workspace.numel(),
+        _current_stream()), "moe_expert_swiglu_fp8")
+    return expert_out
+
+
+def layer_workspace_bytes(shape: Shape, I: int) -> int:
+    return int(lib().moe_layer_workspace_bytes(ctypes.byref(shape.c()), I))
+
+
+def layer(logits: torch.Tensor, x: torch.Tensor, k: int, w_gate_up: torch.Tensor,
+          w_down: torch.Tensor, s_gate_up: torch.Tensor | None = None,
+          s_down: torch.Tensor | None = None, topk_idx: torch.Tensor | None = None,
+          topk_w: torch.Tensor | None = None, y: torch.Tensor | None = None,
+          workspace: torch.Tensor | None = None):
+    """The whole MoE layer of a few tokens (T <= 128, T * k <= 1024): routing,
+    SwiGLU experts and combine of x [T, H] bfloat16. Weights [E, 2I, H] and
+    [E, H, I] bfloat16, or float8_e4m3fn with their 128 x 128 block scales.
+    Returns (y bfloat16 [T, H], topk_idx int32 [T, k], topk_w float32 [T, k])."""
+    if logits.dim() != 2 or x.dim() != 2 or w_down.dim() != 3:
+        raise ValueError("logits must be [T, E], x [T, H] and w_down [E, H, I]")
+    T, E = logits.shape
+    H, I = x.shape[1], w_down.shape[2]
+    f32, bf16 = torch.float32, torch.bfloat16
+    fp8 = w_down.dtype == _FP8
+    if fp8 and (s_gate_up is None or s_down is None):
+        raise ValueError("8-bit weights need s_gate_up and s_down")
+    wtype = _FP8 if fp8 else bf16
+    dev = x.device
+    topk_idx = _empty((T, k), torch.int32, dev) if topk_idx is None else topk_idx
+    topk_w = _empty((T, k), f32, dev) if topk_w is None else topk_w
+    y = _empty((T, H), bf16, dev) if y is None else y
+    sh = ctypes.byref(MoeShape(T, H, E, k, 1, 1, MOE_BF16))
+    if workspace is None:
+        workspace = _workspace(None, int(lib().moe_layer_workspace_bytes(sh, I)), dev)
+    _check(lib().moe_layer(
+        sh, I, MOE_F8E4M3 if fp8 else MOE_BF16, _checked("logits", logits, (T, E), f32),
+        _checked("x", x, (T, H), bf16), _checked("w_gate_up", w_gate_up, (E, 2 * I, H), wtype),
+        _checked("s_gate_up", s_gate_up, (E, _blocks(2 * I), _blocks(H)), f32) if fp8 else None,
+        _checked("w_down", w_down, (E, H, I), wtype),
+        _checked("s_down", s_down, (E, _blocks(H), _blocks(I)), f32) if fp8 else None,
+        _checked("topk_idx", topk_idx, (T, k), torch.int32), _checked("topk_w", topk_w, (T, k), f32),
+        _checked("y", y, (T, H), bf16),
+        _checked("workspace", workspace, tuple(workspace.shape), torch.uint8), workspace.numel(),
+        _current_stream()), "moe_layer")
+    return y, topk_idx, topk_w
 
 
 # ---------------------------------------------------------------------- stats

@@ -739,7 +739,152 @@ void* scratch_on_current_device() {
 
 }  // namespace
 
+// ------------------------------------------------- 8-bit experts, small layer
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round256(int64_t b) { return (b < 256 ? 256 : ceil_div(b, 256) * 256); }
+
+// One expert's weights and one 256-row tile are addressed through buffer
+// descriptors with 31-bit byte ranges; the tile list with 32-bit numbers.
+int check_gemm_fp8_sizes(int64_t rows, int64_t E, int64_t N, int64_t K) {
+  if (rows < 0 || rows >= kIndexLimit || E < 1 || E > 1024 || N < 16 || N % 16 != 0 || K < 128 ||
+      K % 128 != 0)
+    return MOE_ERR_ARG;
+  if (N * K >= (int64_t(1) << 31) || 256 * K >= (int64_t(1) << 31) || 512 * N >= (int64_t(1) << 31))
+    return MOE_ERR_ARG;
+  if (E * N * K >= (int64_t(1) << 40)) return MOE_ERR_ARG;
+  const int64_t mtiles = rows / 32 + (rows < E ? rows : E);
+  if (mtiles * ceil_div(N, 128) >= (int64_t(1) << 30)) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+int check_layer_shape(const moe_shape* sh, int32_t I) {
+  const int st = check_shape(sh);
+  if (st != MOE_OK) return st;
+  if (sh->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (sh->T > moe::kLayerMaxT || int64_t(sh->T) * sh->k > moe::kLayerMaxPicks) return MOE_ERR_ARG;
+  if (I < 64 || I % 64 != 0 || sh->H % 128 != 0) return MOE_ERR_ARG;
+  if (int64_t(sh->E) * 2 * I * sh->H >= (int64_t(1) << 40)) return MOE_ERR_ARG;
+  if (int64_t(moe::kLayerMaxPicks) * I >= kIndexLimit) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+int moe_quantize(const void* x, int32_t dtype, int32_t batch, int32_t rows, int32_t cols,
+                 int32_t block_rows, void* q, float* scale, moe_stream_t stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (batch < 0 || rows < 0 || cols < 1 || (block_rows != 1 && block_rows != 128))
+    return MOE_ERR_ARG;
+  if (cols % 16 != 0) return MOE_ERR_ALIGN;
+  // 16-element vectors are counted in 32 bits
+  const int64_t vecs = 8 * ceil_div(cols, 128);
+  if (int64_t(batch) * rows >= kIndexLimit || int64_t(batch) * rows * vecs >= kIndexLimit)
+    return MOE_ERR_ARG;
+  if (batch > 0 && rows > 0 && (!x || !q || !scale)) return MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_ALIGN;
+  return status_of(
+      moe::launch_quantize(x, dtype, batch, rows, cols, block_rows, q, scale, as_stream(stream)));
+}
+
+int moe_dispatch_copy_fp8(const moe_shape* shape, const void* x, const int32_t* pos, void* send_q,
+                          float* send_scale, moe_stream_t stream) {
+  const int st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (shape->H % 16 != 0) return MOE_ERR_ALIGN;
+  if (int64_t(shape->T) * 8 * ceil_div(shape->H, 128) >= kIndexLimit) return MOE_ERR_ARG;
+  if (shape->T > 0 && (!x || !pos || !send_q || !send_scale)) return MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(send_q, 16) || !aligned(pos, 4) || !aligned(send_scale, 4))
+    return MOE_ERR_ALIGN;
+  return status_of(moe::launch_dispatch_fp8(x, shape->dtype, pos, shape->T, shape->k, shape->H,
+                                            int64_t(shape->T) * shape->k, send_q, send_scale,
+                                            as_stream(stream)));
+}
+
+int moe_expert_gemm_fp8(int32_t rows, int32_t E, int32_t N, int32_t K, const void* a,
+                        const float* a_scale, const int32_t* expert_offsets,
+                        const int32_t* expert_counts, const void* w, const float* w_scale,
+                        void* out, moe_stream_t stream) {
+  const int st = check_gemm_fp8_sizes(rows, E, N, K);
+  if (st != MOE_OK) return st;
+  if (!expert_offsets || !expert_counts || !w || !w_scale) return MOE_ERR_ARG;
+  if (rows > 0 && (!a || !a_scale || !out)) return MOE_ERR_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(a_scale, 4) ||
+      !aligned(w_scale, 4) || !aligned(expert_offsets, 4) || !aligned(expert_counts, 4))
+    return MOE_ERR_ALIGN;
+  return status_of(moe::launch_gemm_fp8(a, a_scale, rows, E, expert_offsets, expert_counts, w,
+                                        w_scale, N, K, out, as_stream(stream)));
+}
+
+size_t moe_expert_swiglu_fp8_workspace_bytes(const moe_shape* shape, int32_t I) {
+  if (check_shape(shape) != MOE_OK || I < 128 || I % 128 != 0) return 0;
+  const int64_t rows = int64_t(shape->T) * shape->k;
+  return size_t(round256(rows * I) + round256(rows * (I / 128) * 4));
+}
+
+int moe_expert_swiglu_fp8(const moe_shape* shape, int32_t I, const void* send_q,
+                          const float* send_scale, const int32_t* expert_offsets,
+                          const int32_t* expert_counts, const void* w_gate_up,
+                          const float* s_gate_up, const void* w_down, const float* s_down,
+                          void* expert_out, void* workspace, size_t workspace_bytes_given,
+                          moe_stream_t stream) {
+  int st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (shape->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (I < 128 || I % 128 != 0 || shape->H % 128 != 0 || I >= (1 << 24)) return MOE_ERR_ARG;
+  const int64_t rows = int64_t(shape->T) * shape->k;
+  if ((st = check_gemm_fp8_sizes(rows, shape->E, int64_t(2) * I, shape->H)) != MOE_OK) return st;
+  if ((st = check_gemm_fp8_sizes(rows, shape->E, shape->H, I)) != MOE_OK) return st;
+  if (!expert_offsets || !expert_counts || !w_gate_up || !s_gate_up || !w_down || !s_down ||
+      !workspace)
+    return MOE_ERR_ARG;
+  if (rows > 0 && (!send_q || !send_scale || !expert_out)) return MOE_ERR_ARG;
+  if (!aligned(send_q, 16) || !aligned(expert_out, 16) || !aligned(w_gate_up, 16) ||
+      !aligned(w_down, 16) || !aligned(workspace, 16) || !aligned(send_scale, 4) ||
+      !aligned(s_gate_up, 4) || !aligned(s_down, 4) || !aligned(expert_offsets, 4) ||
+      !aligned(expert_counts, 4))
+    return MOE_ERR_ALIGN;
+  if (workspace_bytes_given < moe_expert_swiglu_fp8_workspace_bytes(shape, I))
+    return MOE_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  return status_of(moe::launch_expert_swiglu_fp8(
+      send_q, send_scale, rows, shape->H, I, shape->E, expert_offsets, expert_counts, w_gate_up,
+      s_gate_up, w_down, s_down, ws, reinterpret_cast<float*>(ws + round256(rows * I)), expert_out,
+      as_stream(stream)));
+}
+
+size_t moe_layer_workspace_bytes(const moe_shape* shape, int32_t I) {
+  if (check_layer_shape(shape, I) != MOE_OK) return 0;
+  return size_t(round256(int64_t(shape->T) * shape->k * I * 2) +
+                round256(4 * moe::layer_plan_ints(shape->T, shape->E, shape->k)));
+}
+
+int moe_layer(const moe_shape* shape, int32_t I, int32_t weight_dtype, const float* logits,
+              const void* x, const void* w_gate_up, const float* s_gate_up, const void* w_down,
+              const float* s_down, int32_t* topk_idx, float* topk_w, void* y, void* workspace,
+              size_t workspace_bytes_given, moe_stream_t stream) {
+  const int st = check_layer_shape(shape, I);
+  if (st != MOE_OK) return st;
+  if (weight_dtype != MOE_BF16 && weight_dtype != MOE_F8E4M3) return MOE_ERR_UNSUPPORTED;
+  const bool fp8 = weight_dtype == MOE_F8E4M3;
+  if (fp8 && I % 128 != 0) return MOE_ERR_ARG;
+  if (!w_gate_up || !w_down || !workspace || (fp8 && (!s_gate_up || !s_down))) return MOE_ERR_ARG;
+  if (shape->T > 0 && (!logits || !x || !topk_idx || !topk_w || !y)) return MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w_gate_up, 16) || !aligned(w_down, 16) ||
+      !aligned(workspace, 16) || !aligned(logits, 4) || !aligned(topk_idx, 4) ||
+      !aligned(topk_w, 4) || !aligned(s_gate_up, 4) || !aligned(s_down, 4))
+    return MOE_ERR_ALIGN;
+  if (workspace_bytes_given < moe_layer_workspace_bytes(shape, I)) return MOE_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  const int64_t hbytes = round256(int64_t(shape->T) * shape->k * I * 2);
+  return status_of(moe::launch_layer(logits, x, shape->T, shape->H, shape->E, shape->k, I, fp8,
+                                     w_gate_up, s_gate_up, w_down, s_down, topk_idx, topk_w, ws,
+                                     reinterpret_cast<int32_t*>(ws + hbytes), y,
+                                     as_stream(stream)));
+}
 
 size_t moe_noalloc_scratch_bytes(void) { return kScratchBytes; }
 

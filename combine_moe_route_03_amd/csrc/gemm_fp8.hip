@@ -1,0 +1,440 @@
+// gemm_fp8.hip -- grouped products of 8-bit rows with 8-bit expert weights, each
+// operand e4m3 with an fp32 scale per block of 128 (rows: 1 x 128, weights:
+// 128 x 128), and the SwiGLU expert FFN made of two of them (expert compute on
+// each expert's contiguous rows: MoE systems survey section 1.1, EP flow step
+// 3; variable-size batched GEMMs driven by the counts, survey section 4.1).
+//
+//   product    out[m][n] = bf16( sum_b sa[m][b] sw[n/128][b] P_b[m][n] ),
+//              P_b[m][n] = sum over the 128 columns j of block b of a[m][j] w[n][j]
+//   gate/up    g, u as above; h = SiLU(g) u; hq, hs = the row quantisation of h
+//              (quant.h), written instead of a bf16 intermediate
+//
+// v_mfma_f32_16x16x128_f8f6f4 makes one P_b for 16 x 16 outputs in one
+// instruction, started from zero, and the vector unit folds it into the fp32
+// accumulators with one fused multiply-add an output while the next product
+// runs, so any fp32 scales are served. Inside, the instruction aligns each run
+// of 8 products to the largest and drops what lies below 2^-13 of it, then adds
+// the runs in fp32 (observed; the 16x16x32 form does the same): a run is off by
+// at most 2^-10 of its magnitudes, of either sign, which is far below the 2^-4
+// the operands were rounded by and, over K, below the rounding to bf16 that
+// follows. Widening to bf16 would keep those bits at half the matrix rate. The
+// weights are the first operand: a lane then holds four outputs of ONE row m
+// (n = 4 (lane / 16) + 0..3, m = lane % 16), so the row scale is one register
+// a lane, the weight scale is uniform, and stores are 16 bytes a lane.
+#include <type_traits>
+
+#include "device.h"
+#include "ffn_device.h"
+#include "launch.h"
+#include "quant.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBK = 128;    // K step: one scale block, one 128-byte tile row
+constexpr int kGroupM = 4;  // m-tiles per rasterisation patch
+
+// LDS tile: rows of 128 bytes = eight 16-byte chunks; chunk c of row r sits at
+// chunk c ^ key(r), so that the 16 lanes that read one chunk column of a
+// fragment in the same cycle hit distinct banks (two rows span the 64 banks).
+// A fragment's rows are 16 consecutive ones. B fragments come in pairs over 32
+// rows, fragment h of a pair taking rows 8 (i / 4) + 4 h + i % 4, i = 0..15:
+// a lane's four outputs of both are then eight consecutive columns.
+__device__ __forceinline__ int a_key(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int b_key(int r) { return ((r >> 1) & 1) | (((r >> 3) & 3) << 1); }
+
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff,
+                                         int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff,
+                                          int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)lds, 4, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
+  // format 0 = e4m3 for both; zero scale operands select the unscaled form
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+
+struct Tile {
+  int e, row0, rows, ntile;  // e < 0: no tile for this block
+};
+
+// Block -> tile. The tiles of all experts, in patches of kGroupM m-tiles by all
+// n-tiles, form one list; workgroups are dealt to the 8 XCDs round-robin and
+// each XCD takes one contiguous share of the list, so it reads its rows and
+// weights through its own L2 (a list of tiles rather than of m-tiles, so that
+// one expert's few rows still spread over all XCDs). Counts that leave [0,
+// rows_total) give no tile. Called by the whole block; info: 4 ints of LDS.
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offs,
+                                          const int32_t* __restrict__ cnts, int E,
+                                          int64_t rows_total, int ntiles, int* info) {
+  const int lane = threadIdx.x & (kWave - 1);
+  if (threadIdx.x < kWave) {
+    if (lane == 0) info[0] = -1;
+    const int c = (E + kWave - 1) / kWave;  // lane l scans experts [l*c, l*c + c)
+    const int e0 = lane * c, e1 = (e0 + c < E) ? e0 + c : E;
+    const auto mtiles = [&](int e) {
+      const int n = cnts[e];
+      return n > 0 && n <= rows_total ? (n + BM - 1) / BM : 0;
+    };
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += mtiles(e);
+    int incl = mine;
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int y = __shfl_up(incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int MT = __shfl(incl, kWave - 1);
+    const int total = MT * ntiles;
+    const int per = (total + kXCD - 1) / kXCD;
+    const int slot = blockIdx.x / kXCD;
+    const int lin = (blockIdx.x % kXCD) * per + slot;
+    if (slot < per && lin < total) {
+      const int grp = lin / (kGroupM * ntiles), r = lin - grp * kGroupM * ntiles;
+      const int gh = MT - grp * kGroupM < kGroupM ? MT - grp * kGroupM : kGroupM;
+      const int ntile = r / gh, mt = grp * kGroupM + (r - ntile * gh);
+      int base = incl - mine;
+      if (mt >= base && mt < incl) {
+        for (int e = e0; e < e1; ++e) {
+          const int n = mtiles(e);
+          if (mt < base + n) {
+            const int m0 = (mt - base) * BM;
+            const int rows = cnts[e] - m0;
+            const int64_t first = (int64_t)offs[e] + m0;
+            if (first >= 0 && first + (rows < BM ? rows : BM) <= rows_total) {
+              info[0] = e;
+              info[1] = (int)first;
+              info[2] = rows < BM ? rows : BM;
+              info[3] = ntile;
+            }
+            break;
+          }
+          base += n;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  return {__builtin_amdgcn_readfirstlane(info[0]), __builtin_amdgcn_readfirstlane(info[1]),
+          __builtin_amdgcn_readfirstlane(info[2]), __builtin_amdgcn_readfirstlane(info[3])};
+}
+
+// BM x BN block tile of WM x WN waves, each (BM/WM) x (BN/WN) as MI x NI
+// fragments of 16 x 16. N: rows of one expert's B (2 I for gate/up).
+template <bool kGateUp, int BM, int BN, int OCC, int WM, int WN>
+__global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
+    const uint8_t* __restrict__ A, const float* __restrict__ Asc,
+    const int32_t* __restrict__ offs, const int32_t* __restrict__ cnts, int E,
+    int64_t rows_total, const uint8_t* __restrict__ B, const float* __restrict__ Bsc, int N, int K,
+    void* __restrict__ C, float* __restrict__ Csc, int ntiles) {
+  constexpr int NW = WM * WN;
+  constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
+  constexpr int AI = BM / NW / 8, BI = BN / NW / 8;  // 1 KiB loads per wave per K step
+  constexpr int kStage = (BM + BN) * kBK + BM * 4;   // A, B, A scales
+  constexpr int NO = kGateUp ? BN / 2 : BN;          // output columns of a tile
+  static_assert(AI >= 1 && BI >= 1 && BM % 64 == 0 && BN / WN <= 128, "tile shape");
+  static_assert(!kGateUp || (NO == kQuantBlock && NI % 4 == 0), "one scale block of h per tile");
+  // separate arrays: the loads into one stage and the reads of the other do not alias
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[kStage];
+  __shared__ int info[4];
+  const auto stage = [&](auto S) -> uint8_t* {
+    if constexpr (decltype(S)::value % 2 == 0) return lds0;
+    else return lds1;
+  };
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wm = wid / WN, wn = wid % WN;
+  const Tile tile = find_tile<BM>(offs, cnts, E, rows_total, ntiles, info);
+  if (tile.e < 0) return;  // uniform over the block
+  const int e = tile.e, row0 = tile.row0, rows = tile.rows, ntile = tile.ntile;
+  // waves whose rows all lie past the tile's last one only load and meet the barriers
+  const bool live = wm * (BM / WM) < rows;
+  const int KB = K / kBK, I = N / 2, NB = (N + kQuantBlock - 1) / kQuantBlock;
+
+  // ---- loads: one wave instruction fills eight 128-byte tile rows, lane l the
+  // slot l % 8 of row l / 8; rows past the last one are out of the descriptor's
+  // range and read as zeros.
+  const __amdgpu_buffer_rsrc_t arsrc = make_rsrc(A + (int64_t)row0 * K, (int64_t)rows * K);
+  const __amdgpu_buffer_rsrc_t brsrc = make_rsrc(B + (int64_t)e * N * K, (int64_t)N * K);
+  const __amdgpu_buffer_rsrc_t srsrc =
+      make_rsrc(Asc + (int64_t)row0 * KB, (int64_t)rows * KB * 4);
+  uint32_t aoff[AI], boff[BI];
+#pragma unroll
+  for (int i = 0; i < AI; ++i) {
+    const int r = wid * (BM / NW) + 8 * i + (lane >> 3);
+    aoff[i] = (uint32_t)r * (uint32_t)K + (((lane & 7) ^ a_key(r)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < BI; ++i) {
+    const int r = wid * (BN / NW) + 8 * i + (lane >> 3);
+    int n;
+    if constexpr (kGateUp) n = r < NO ? ntile * NO + r : I + ntile * NO + (r - NO);
+    else n = ntile * BN + r;
+    boff[i] = (uint32_t)n * (uint32_t)K + (((lane & 7) ^ b_key(r)) << 4);
+  }
+  const int srow = wid % (BM / 64) * 64;  // the 64 row scales this wave loads
+  const uint32_t soff = (uint32_t)(srow + lane) * (uint32_t)KB * 4;
+  constexpr int kLoads = AI + BI + 1;
+  auto issue = [&](uint8_t* st, int kt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+      load_lds(arsrc, st + (wid * (BM / NW) + 8 * i) * kBK, aoff[i], kt * kBK);
+#pragma unroll
+    for (int i = 0; i < BI; ++i)
+      load_lds(brsrc, st + (BM + wid * (BN / NW) + 8 * i) * kBK, boff[i], kt * kBK);
+    load_lds4(srsrc, st + (BM + BN) * kBK + srow * 4, soff, kt * 4);
+  };
+
+  // ---- fragments: lane l holds row (l % 16), chunks 2 (l / 16) and the next
+  // of its 128 bytes (both operands alike, so the order of k does not matter)
+  const int fi = lane & 15, fc = (lane >> 4) * 2;
+  const int arow = wm * (BM / WM) + fi;
+  const int a0 = arow * kBK + ((fc ^ a_key(arow)) << 4);
+  const int a1 = arow * kBK + (((fc + 1) ^ a_key(arow)) << 4);
+  const int brow = (kGateUp ? wn * (NO / WN) : wn * (BN / WN)) + 8 * (fi >> 2) + (fi & 3);
+  const int b0 = (BM + brow) * kBK + ((fc ^ b_key(brow)) << 4);
+  const int b1 = (BM + brow) * kBK + (((fc + 1) ^ b_key(brow)) << 4);
+  auto frag = [&](const uint8_t* st, int o0, int o1, int off) __attribute__((always_inline)) -> i32x8 {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(st + o0 + off);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(st + o1 + off);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto read_a = [&](const uint8_t* st, int mi) { return frag(st, a0, a1, mi * 16 * kBK); };
+  auto read_b = [&](const uint8_t* st, int ni) {
+    // rows of fragment ni past this wave's first: pairs of 32, four apart inside
+    const int q = kGateUp ? ni % (NI / 2) : ni;
+    const int r = 32 * (q >> 1) + 4 * (q & 1) + (kGateUp && ni >= NI / 2 ? NO : 0);
+    return frag(st, b0, b1, r * kBK);
+  };
+  auto read_s = [&](const uint8_t* st, int mi) -> float {
+    return *reinterpret_cast<const float*>(st + (BM + BN) * kBK + (arow + mi * 16) * 4);
+  };
+
+  // Weight scales of this wave's column block(s): lane l holds K block kt0 + l,
+  // read out by lane index, reloaded every 64 steps.
+  const int ncol = ntile * NO + wn * (NO / WN);  // first output column of the wave
+  int nb0 = ncol / kQuantBlock;
+  if (nb0 > NB - 1) nb0 = NB - 1;
+  const float* bs0 = Bsc + ((int64_t)e * NB + nb0) * KB;
+  const float* bs1 = kGateUp ? bs0 + (int64_t)(I / kQuantBlock) * KB : bs0;
+  float sv0 = 0.f, sv1 = 0.f;
+  auto load_bs = [&](int kt0) __attribute__((always_inline)) {
+    const int i = kt0 + lane < KB ? kt0 + lane : KB - 1;
+    sv0 = bs0[i];
+    if constexpr (kGateUp) sv1 = bs1[i];
+  };
+  auto lane_f = [&](float v, int l) {
+    return __uint_as_float(lane_value(__float_as_uint(v), l));
+  };
+
+  f32x4 acc[NI][MI];
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) acc[ni][mi] = f32x4{0, 0, 0, 0};
+
+  i32x8 fa[MI], fb[2];
+  float sa[MI];
+  load_bs(0);
+  issue(lds0, 0);
+  issue(lds1, KB > 1 ? 1 : 0);
+  __builtin_amdgcn_s_waitcnt(wait_vmcnt(kLoads));
+  __syncthreads();
+
+  // Step kt reads stage kt % 2. Its fragments of A, the row scales and the first
+  // fragment of B are in registers already. Before the last column of MFMAs,
+  // this wave's loads of step kt+1 have landed; one barrier (every wave has
+  // read the whole stage); then step kt+2 is loaded into it and the first
+  // fragments of step kt+1 are read while the last MFMAs run. Past the last
+  // step the loads repeat it into a stage nobody reads again.
+  auto step = [&](auto S, int kt) __attribute__((always_inline)) {
+    uint8_t* cur = stage(S);
+    const uint8_t* nxt = stage(std::integral_constant<int, decltype(S)::value + 1>{});
+    if ((kt & 63) == 0 && kt > 0) {
+      load_bs(kt);
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    }
+    const float w0 = lane_f(sv0, kt & 63), w1 = kGateUp ? lane_f(sv1, kt & 63) : 0.f;
+    float s0[MI], s1[MI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      s0[mi] = sa[mi] * w0;
+      s1[mi] = kGateUp ? sa[mi] * w1 : s0[mi];
+    }
+    f32x4 t[2][MI];
+    auto fold = [&](int ni) __attribute__((always_inline)) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[ni][mi][r] = __builtin_fmaf(t[ni & 1][mi][r],
+                                          kGateUp && ni >= NI / 2 ? s1[mi] : s0[mi], acc[ni][mi][r]);
+    };
+#pragma unroll
+    for (int ni = 0; ni < NI - 1; ++ni) {
+      fb[(ni + 1) & 1] = read_b(cur, ni + 1);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) t[ni & 1][mi] = mfma_fp8(fb[ni & 1], fa[mi]);
+      if (ni > 0) fold(ni - 1);
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+    issue(cur, kt + 2 < KB ? kt + 2 : KB - 1);
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      t[(NI - 1) & 1][mi] = mfma_fp8(fb[(NI - 1) & 1], fa[mi]);
+      fa[mi] = read_a(nxt, mi);
+      sa[mi] = read_s(nxt, mi);
+    }
+    fb[0] = read_b(nxt, 0);
+    fold(NI - 2);
+    fold(NI - 1);
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  if (live) {
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      fa[mi] = read_a(lds0, mi);
+      sa[mi] = read_s(lds0, mi);
+    }
+    fb[0] = read_b(lds0, 0);
+    int kt = 0;
+    for (; kt + 2 <= KB; kt += 2) {
+      step(I0{}, kt);
+      step(I1{}, kt + 1);
+    }
+    if (kt < KB) step(I0{}, kt);
+  } else {
+    for (int kt = 0; kt < KB; ++kt) {
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+      __syncthreads();
+      issue(kt & 1 ? lds1 : lds0, kt + 2 < KB ? kt + 2 : KB - 1);
+    }
+  }
+  // the trailing loads must land before the block's LDS is reused or released
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+
+  // ---- epilogue: the stores go through descriptors over the tile's rows, whose
+  // range check drops the rows past the last one.
+  const int g = lane >> 4;
+  if constexpr (!kGateUp) {
+    if (!live) return;
+    const __amdgpu_buffer_rsrc_t crsrc =
+        make_rsrc(static_cast<uint16_t*>(C) + (int64_t)row0 * N, (int64_t)rows * N * 2);
+#pragma unroll
+    for (int p = 0; p < NI / 2; ++p) {
+      const int n = ncol + 32 * p + 8 * g;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
+        const v4u v = {bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]),
+                       bf16x2_rne(hi[0], hi[1]), bf16x2_rne(hi[2], hi[3])};
+        // columns past N would wrap into the next row: offset out of range instead
+        const uint32_t off = n < N ? ((uint32_t)(arow + mi * 16) * (uint32_t)N + n) * 2 : 0xFFFFFFF0u;
+        __builtin_amdgcn_raw_buffer_store_b128(v, crsrc, off, 0, 0);
+      }
+    }
+  } else {
+    // h = SiLU(g) u in place of g; the row maximum over the tile's 128 columns:
+    // this lane's, the other lanes' of the row (16 and 32 apart), the other
+    // waves' through LDS. Rows are whole scale blocks of h.
+    uint32_t* ex = reinterpret_cast<uint32_t*>(lds0);  // [WN][BM]
+    uint32_t am[MI];
+    __syncthreads();  // every wave is done with the stages
+    if (live) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int ni = 0; ni < NI / 2; ++ni)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float h = silu(acc[ni][mi][r]) * acc[ni + NI / 2][mi][r];
+            acc[ni][mi][r] = h;
+            const uint32_t u = finite_bits(h);
+            m = u > m ? u : m;
+          }
+        uint32_t o = (uint32_t)__shfl_xor((int)m, 16);
+        m = o > m ? o : m;
+        o = (uint32_t)__shfl_xor((int)m, 32);
+        m = o > m ? o : m;
+        if (g == 0) ex[wn * BM + arow + mi * 16] = m;
+      }
+    }
+    __syncthreads();
+    if (!live) return;
+    const __amdgpu_buffer_rsrc_t crsrc =
+        make_rsrc(static_cast<uint8_t*>(C) + (int64_t)row0 * I, (int64_t)rows * I);
+    const int IB = I / kQuantBlock;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const int m = arow + mi * 16;
+      uint32_t a = 0;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) a = ex[w * BM + m] > a ? ex[w * BM + m] : a;
+      am[mi] = a;
+      const int p2 = scale_exponent(am[mi]);
+      const float inv = power_of_two(-p2);
+      if (g == 0 && wn == 0 && m < rows) Csc[(int64_t)(row0 + m) * IB + ntile] = power_of_two(p2);
+#pragma unroll
+      for (int p = 0; p < NI / 4; ++p) {
+        const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
+        const uint32_t q0 = e4m3x4(e4m3_clamp(lo[0] * inv), e4m3_clamp(lo[1] * inv),
+                                   e4m3_clamp(lo[2] * inv), e4m3_clamp(lo[3] * inv));
+        const uint32_t q1 = e4m3x4(e4m3_clamp(hi[0] * inv), e4m3_clamp(hi[1] * inv),
+                                   e4m3_clamp(hi[2] * inv), e4m3_clamp(hi[3] * inv));
+        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(v2u{q0, q1}, crsrc,
+                                              (uint32_t)m * (uint32_t)I + ncol + 32 * p + 8 * g, 0, 0);
+      }
+    }
+  }
+}
+
+template <bool kGateUp, int BM, int BN, int OCC, int WM, int WN>
+hipError_t run_gemm(const void* a, const float* asc, int64_t rows, int E, const int32_t* offs,
+                    const int32_t* cnts, const void* w, const float* wsc, int N, int K, void* c,
+                    float* csc, hipStream_t s) {
+  constexpr int NO = kGateUp ? BN / 2 : BN;
+  const int cols = kGateUp ? N / 2 : N;
+  const int ntiles = (cols + NO - 1) / NO;
+  // every expert with rows adds at most one partial m-tile
+  const int64_t mt = rows / BM + (rows < E ? rows : E);
+  const int64_t per = (mt * ntiles + kXCD - 1) / kXCD;
+  return launch(gemm_fp8_kernel<kGateUp, BM, BN, OCC, WM, WN>, dim3((unsigned)(per * kXCD)),
+                dim3(kWave * WM * WN), 0, s, static_cast<const uint8_t*>(a), asc, offs, cnts, E,
+                rows, static_cast<const uint8_t*>(w), wsc, N, K, c, csc, ntiles);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
+                           const int32_t* offs, const int32_t* cnts, const void* w,
+                           const float* wsc, int N, int K, void* out, hipStream_t s) {
+  if (rows == 0) return hipSuccess;
+  return run_gemm<false, 256, 256, 1, 4, 2>(a, asc, rows, E, offs, cnts, w, wsc, N, K, out, nullptr,
+                                            s);
+}
+
+hipError_t launch_expert_swiglu_fp8(const void* send, const float* ssc, int64_t rows, int H, int I,
+                                    int E, const int32_t* offs, const int32_t* cnts,
+                                    const void* w_gate_up, const float* gsc, const void* w_down,
+                                    const float* dsc, void* hq, float* hs, void* out,
+                                    hipStream_t s) {
+  if (rows == 0) return hipSuccess;
+  const hipError_t err = run_gemm<true, 256, 256, 1, 4, 2>(send, ssc, rows, E, offs, cnts,
+                                                           w_gate_up, gsc, 2 * I, H, hq, hs, s);
+  if (err != hipSuccess) return err;
+  return launch_gemm_fp8(hq, hs, rows, E, offs, cnts, w_down, dsc, H, I, out, s);
+}
+
+}  // namespace moe

@@ -219,6 +219,36 @@ hipError_t launch_expert_swiglu_subset(const void* send, int64_t rows, int H, in
                                        const int32_t* cnts, const void* w_gate_up,
                                        const void* w_down, void* hbuf, void* out, hipStream_t s);
 
+// 8-bit block quantisation (e4m3, power-of-two scales): x [batch][rows][cols],
+// blocks of block_rows (1 or 128) x 128; cols % 16 == 0.
+hipError_t launch_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int cols,
+                           int block_rows, void* q, float* scale, hipStream_t s);
+// The dispatch copy with the rows quantised on the way; H % 16 == 0.
+hipError_t launch_dispatch_fp8(const void* x, int dtype, const int32_t* pos, int T, int k, int H,
+                               int64_t send_rows, void* send_q, float* send_scale, hipStream_t s);
+// Grouped product of 8-bit rows and weights [E][N][K] into bf16 rows of N;
+// K % 128 == 0, N % 16 == 0.
+hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
+                           const int32_t* offs, const int32_t* cnts, const void* w,
+                           const float* wsc, int N, int K, void* out, hipStream_t s);
+// The SwiGLU FFN on 8-bit rows: gate/up product with SiLU, u and the row
+// quantisation of h fused into hq [rows][I] and hs [rows][I/128], then the down
+// product. H % 128 == 0, I % 128 == 0.
+hipError_t launch_expert_swiglu_fp8(const void* send, const float* ssc, int64_t rows, int H, int I,
+                                    int E, const int32_t* offs, const int32_t* cnts,
+                                    const void* w_gate_up, const float* gsc, const void* w_down,
+                                    const float* dsc, void* hq, float* hs, void* out,
+                                    hipStream_t s);
+// The MoE layer of a few tokens (T <= kLayerMaxT, T*k <= 1024): routing, gate/up
+// into h [T*k][I] bf16, down and combine into y. plan: layer_plan_ints int32.
+constexpr int kLayerMaxT = 128;
+constexpr int kLayerMaxPicks = 1024;
+int64_t layer_plan_ints(int T, int E, int k);
+hipError_t launch_layer(const float* logits, const void* x, int T, int H, int E, int k, int I,
+                        bool fp8, const void* w_gate_up, const float* s_gate_up,
+                        const void* w_down, const float* s_down, int32_t* topk_idx, float* topk_w,
+                        void* h, int32_t* plan, void* y, hipStream_t s);
+
 // The gather dispatch of wave w's rows: send[r] = x[row_token[r]] for r in
 // [wave_offsets[w], wave_offsets[w+1]) (read on the device).
 hipError_t launch_gather_wave(const void* x, const int32_t* row_token, const int32_t* wave_offsets,
