@@ -766,7 +766,10 @@ int check_layer_shape(const moe_shape* sh, int32_t I) {
   if (sh->T > moe::kLayerMaxT || int64_t(sh->T) * sh->k > moe::kLayerMaxPicks) return MOE_ERR_ARG;
   if (I < 64 || I % 64 != 0 || sh->H % 128 != 0) return MOE_ERR_ARG;
   if (int64_t(sh->E) * 2 * I * sh->H >= (int64_t(1) << 40)) return MOE_ERR_ARG;
-  if (int64_t(moe::kLayerMaxPicks) * I >= kIndexLimit) return MOE_ERR_ARG;
+  // one expert's weights, x and h are addressed through 31-bit byte ranges
+  if (int64_t(4) * I * sh->H >= (int64_t(1) << 31) || int64_t(2) * moe::kLayerMaxPicks * I >= (int64_t(1) << 31) ||
+      int64_t(2) * moe::kLayerMaxT * sh->H >= (int64_t(1) << 31))
+    return MOE_ERR_ARG;
   return MOE_OK;
 }
 

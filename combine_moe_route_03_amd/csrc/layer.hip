@@ -31,24 +31,36 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxPicks = 1024;
-constexpr int kRouteT = 4;  // most tokens that every gate/up block routes itself
 constexpr int kMaxE = 1024;
-constexpr int kUpWaves = 4;    // waves of a gate/up block: each takes every fourth K step
-constexpr int kUpCols = 8;     // intermediate columns of a gate/up block (8 gate + 8 up rows)
-constexpr int kDownWaves = 8;  // waves of a down block: each takes one range of K steps
-constexpr int kDownCols = 16;  // output columns of a down block
+constexpr int kRouteT = 8;     // most tokens that every gate/up block routes itself
+constexpr int kUpWaves = 4;    // waves of a gate/up block
+constexpr int kUpCols = 8;     // intermediate columns of a unit (8 gate + 8 up rows)
 
 // The live experts in id order and their picks: what both launches need of the
-// routing. In the workspace and, while it is built, in LDS.
+// routing. A pass over an expert's weights serves kGroup picks, so an expert
+// with more is listed 2 or 4 times (its "parts"), and each list entry ("slot") is
+// one word: expert, first entry in pick, part, picks of the expert (0: no slot).
+constexpr int kGroup = 32;
+__host__ __device__ __forceinline__ int parts_of(int cnt) { return cnt <= 32 ? 1 : (cnt <= 64 ? 2 : 4); }
+__device__ __forceinline__ uint32_t slot_word(int e, int first, int part, int cnt) {
+  return (uint32_t)e | (uint32_t)first << 10 | (uint32_t)part << 20 | (uint32_t)cnt << 22;
+}
+__device__ __forceinline__ int slot_expert(uint32_t s) { return s & 1023; }
+__device__ __forceinline__ int slot_first(uint32_t s) { return (s >> 10) & 1023; }
+__device__ __forceinline__ int slot_part(uint32_t s) { return (s >> 20) & 3; }
+__device__ __forceinline__ int slot_count(uint32_t s) { return s >> 22; }
+static_assert(kMaxE <= 1024 && kMaxPicks <= 1024 && kLayerMaxT <= 4 * kGroup, "fields of a slot word");
+// Most slots: one an expert, and up to three more for 65 picks (one for 33).
+__host__ __device__ constexpr int max_slots(int E, int np) { return (np < E ? np : E) + np / 21; }
+
 struct Plan {
-  int32_t* n;       // live experts ("slots")
-  int32_t* expert;  // [slots]
-  int32_t* first;   // [slots + 1] first entry of each slot in pick
-  int32_t* pick;    // [T*k] picks (t * k + i) grouped by slot
+  int32_t* n;      // slots in use
+  uint32_t* slot;  // [slots], zero past those in use
+  int32_t* pick;   // [T*k] picks (t * k + i) grouped by slot
 };
 
 __host__ __device__ __forceinline__ Plan plan_at(int32_t* ws, int slots) {
-  return {ws, ws + 4, ws + 4 + slots, ws + 4 + 2 * slots + 1};
+  return {ws, reinterpret_cast<uint32_t*>(ws + 4), ws + 4 + slots};
 }
 
 template <int NP>  // most picks
@@ -56,47 +68,55 @@ struct PlanLds {
   int32_t idx[NP];     // expert of each pick
   int32_t pick[NP];    // picks grouped by slot
   int32_t cur[kMaxE];  // counts, then the next free entry of each expert
-  int32_t expert[NP];
-  int32_t first[NP + 1];
+  uint32_t slot[max_slots(NP, NP)];
   int32_t part[16];
   int32_t n;
 };
 
-// Routes all T tokens (one wave a token at a time, V >= E / 64 logits a lane)
-// and groups the picks, all in one block of NT threads. The order of the picks
-// inside a slot is not fixed (LDS atomics), and nothing depends on it: a pick
-// is a column of a matrix product and goes to a token of its own.
+// Routes all T tokens (G lanes a token, V >= E / G logits a lane; V = 0: reads
+// the picks of an earlier launch) and groups the picks, all in one block of NT
+// threads. The order of the picks inside a
+// slot is not fixed (LDS atomics), and nothing depends on it: a pick is a
+// column of a matrix product and goes to a token of its own. publish: this
+// block also writes the plan, the picks and weights.
 template <int NT, int V, int NP>
 __device__ __forceinline__ void route_and_plan(PlanLds<NP>& P, const float* __restrict__ logits, int T,
-                                               int E, int k, bool publish,
+                                               int E, int k, int G, bool publish,
                                                int32_t* __restrict__ topk_idx,
-                                               float* __restrict__ topk_w, const Plan& out) {
+                                               float* __restrict__ topk_w, const Plan& out,
+                                               int slots) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wid = tid / kWave;
   constexpr int NW = NT / kWave;
   for (int e = tid; e < E; e += NT) P.cur[e] = 0;
-  for (int t = wid; t < T; t += NW) {
-    int id;
-    float w;
-    route_token<V, false>(logits, t, true, E, k, kWave, lane, id, w);
-    if (id >= 0) {
-      P.idx[t * k + lane] = id;
-      if (publish) {
-        topk_idx[t * k + lane] = id;
-        topk_w[t * k + lane] = w;
+  const int np = T * k;
+  if constexpr (V > 0) {
+    const int g = lane & (G - 1), per_pass = NT / G;
+    for (int t0 = 0; t0 < T; t0 += per_pass) {
+      const int t = t0 + tid / G;
+      int id;
+      float w;
+      route_token<V, false>(logits, t, t < T, E, k, G, g, id, w);
+      if (id >= 0) {
+        P.idx[t * k + g] = id;
+        if (publish) {
+          topk_idx[t * k + g] = id;
+          topk_w[t * k + g] = w;
+        }
       }
     }
+  } else {
+    for (int p = tid; p < np; p += NT) P.idx[p] = topk_idx[p];
   }
   __syncthreads();
-  const int np = T * k;
   for (int p = tid; p < np; p += NT) atomicAdd(&P.cur[P.idx[p]], 1);
   __syncthreads();
-  // exclusive scan over the experts of (live << 16) + count
+  // exclusive scan over the experts of (slots << 16) + picks
   const int per = (E + NT - 1) / NT;
   int mine = 0;
   for (int j = 0; j < per; ++j) {
     const int e = tid * per + j;
     const int c = e < E ? P.cur[e] : 0;
-    mine += c > 0 ? (1 << 16) + c : 0;
+    mine += c > 0 ? (parts_of(c) << 16) + c : 0;
   }
   int incl = mine;
   for (int o = 1; o < kWave; o <<= 1) {
@@ -114,24 +134,20 @@ __device__ __forceinline__ void route_and_plan(PlanLds<NP>& P, const float* __re
     const int e = tid * per + j;
     const int c = e < E ? P.cur[e] : 0;
     if (c > 0) {
-      P.expert[at >> 16] = e;
-      P.first[at >> 16] = at & 0xFFFF;
+      const int parts = parts_of(c);
+      for (int q = 0; q < parts; ++q) P.slot[(at >> 16) + q] = slot_word(e, at & 0xFFFF, q, c);
       P.cur[e] = at & 0xFFFF;
-      at += (1 << 16) + c;
+      at += (parts << 16) + c;
     }
   }
   const int n = total >> 16;
-  if (tid == 0) {
-    P.n = n;
-    P.first[n] = np;
-  }
+  if (tid == 0) P.n = n;
   __syncthreads();
   for (int p = tid; p < np; p += NT) P.pick[atomicAdd(&P.cur[P.idx[p]], 1)] = p;
   __syncthreads();
   if (publish) {
     if (tid == 0) *out.n = n;
-    for (int s = tid; s < n; s += NT) out.expert[s] = P.expert[s];
-    for (int s = tid; s <= n; s += NT) out.first[s] = P.first[s];
+    for (int s = tid; s < slots; s += NT) out.slot[s] = s < n ? P.slot[s] : 0;
     for (int p = tid; p < np; p += NT) out.pick[p] = P.pick[p];
   }
 }
@@ -147,306 +163,463 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {
   return bf16x8{w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
 }
 
-// One K step is 128 bytes of a weight row: 64 bf16 or 128 e4m3 columns. Lane
-// l takes bytes [32 g, 32 g + 32) of row l % 16, g = l / 16, and the same
-// columns of token l % 16 (the order of k is the same in both operands, so it
-// does not matter which of an instruction's k they are).
+// ---- the weight stream. A unit is 16 (or 8) weight rows; a K step is 128 bytes
+// of each: 64 bf16 or 128 e4m3 columns. Every load instruction takes whole
+// 128-byte lines, lane l chunk l % 8 of row l / 8 (16 bytes a lane): lanes in
+// the order of an MFMA operand, 16 rows by 64 bytes, reached 5.6-6.2 TB/s on the
+// same stream, this order 6.9-7.0. The loads of D steps are in flight in
+// a register ring; a step's registers then go through the wave's own piece of
+// LDS into operand order (no barrier: a wave's LDS operations are in order).
+// Units start at different steps, since weight rows a power of two apart would
+// otherwise have all waves on the same memory channels at one time (5.9 against
+// 6.2-7.0 TB/s).
 template <bool kFp8>
 struct Step {
   static constexpr int kCols = kFp8 ? 128 : 64;
-  static constexpr int kB = kFp8 ? 4 : 2;  // 16-byte token vectors and MFMAs a step
+  static constexpr int kB = kFp8 ? 2 : 1;  // 128-byte pieces of a token row a step
 };
 
-// acc[nt] += the products of this lane's weight row with NT x 16 tokens over
-// the K steps s0, s0 + stride, ... < s1. wp: the lane's weight row at its g
-// offset; xp[nt]: the lane's token rows at theirs. scale0 / scale1 (e4m3):
-// scales of the row blocks of D registers 0-1 and 2-3, one a step.
-template <bool kFp8, int NT, int U>
-__device__ __forceinline__ void dot_steps(const uint8_t* __restrict__ wp,
-                                          const uint16_t* const (&xp)[NT],
-                                          const float* __restrict__ scale0,
-                                          const float* __restrict__ scale1, int s0, int s1,
-                                          int stride, f32x4 (&acc)[NT]) {
-  constexpr int kB = Step<kFp8>::kB;
-  auto group = [&](auto un, int s) __attribute__((always_inline)) {
-    constexpr int N = decltype(un)::value;
-    v4u w[N][2], x[N][NT][kB];
-    float c0[N], c1[N];
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const v4u* p = reinterpret_cast<const v4u*>(wp + (int64_t)(s + u * stride) * 128);
-      w[u][0] = load_stream(p);
-      w[u][1] = load_stream(p + 1);
-    }
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const v4u* p =
-            reinterpret_cast<const v4u*>(xp[nt] + (int64_t)(s + u * stride) * Step<kFp8>::kCols);
-#pragma unroll
-        for (int b = 0; b < kB; ++b) x[u][nt][b] = p[b];
-      }
-      if constexpr (kFp8) {
-        c0[u] = scale0[s + u * stride];
-        c1[u] = scale1[s + u * stride];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      if constexpr (kFp8) {
-        bf16x8 a[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) a[b] = widen8(w[u][b >> 1][2 * (b & 1)], w[u][b >> 1][2 * (b & 1) + 1]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          f32x4 t = {0, 0, 0, 0};
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                a[b], __builtin_bit_cast(bf16x8, x[u][nt][b]), t, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[nt][r] = __builtin_fmaf(t[r], r < 2 ? c0[u] : c1[u], acc[nt][r]);
-        }
-      } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, w[u][b]), __builtin_bit_cast(bf16x8, x[u][nt][b]),
-                acc[nt], 0, 0, 0);
-      }
-    }
-  };
-  int s = s0;
-  for (; s + (U - 1) * stride < s1; s += U * stride) group(std::integral_constant<int, U>{}, s);
-  for (; s < s1; s += stride) group(std::integral_constant<int, 1>{}, s);
+constexpr uint32_t kOutside = 0xFFFFFFF0u;  // byte offset outside every descriptor's range
+constexpr int kStream = 2;                  // cache policy: weights are read once
+
+__device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+}
+__device__ __forceinline__ v4u load16_stream(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStream);
+}
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
 
-// Gate/up: block (unit, slot) computes kUpCols intermediate columns of one live
-// expert for all its picks. MFMA row i is gate row 2 (i / 4) + i % 4 for i % 4
-// < 2, else the up row of the same column, so a lane's four results are g, g,
-// u, u of two neighbouring columns. kV > 0: the block routes all tokens itself
-// (kV logits a lane), block (0, 0) publishes; kV = 0: the plan is in the
-// workspace.
-template <int kV, bool kFp8>
-__global__ __launch_bounds__(kWave * kUpWaves) void layer_gate_up_kernel(
+// Byte offset of 16-byte chunk c of LDS tile row r (rows of 128 bytes): the 16
+// lanes that read one chunk column at a time hit distinct banks.
+__device__ __forceinline__ int tile_at(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
+
+// Bytes of LDS a wave needs for NB groups of 8 tokens, and the steps in flight
+// that fit 168 registers (three waves a SIMD).
+constexpr int stage_bytes(int NB) { return 2048 + NB * 1024; }
+template <bool kFp8, int RW, int NB>
+constexpr int kRing = kFp8 ? (NB == 1 ? (RW == 8 ? 6 : 4) : (NB == 2 ? 3 : 2))
+                           : (NB == 1 ? (RW == 8 ? 8 : 6) : (NB == 2 ? 4 : 3));
+
+// acc[t] += the products of the unit's rows with NB x 8 tokens over n K steps
+// from s0, beginning with step s0 + rot. woff: byte offsets in wr of the lane's two rows at
+// its chunk (RW = 8: the first only), wrow their LDS rows; xoff[b]: in xr of
+// its token of group b at its chunk (kOutside without a token: zeros, no memory
+// access); c0, c1 (e4m3): in cr of the scales of D registers 0-1 and 2-3, one a
+// step. Steps past the last are outside the range, so the loop has no branches.
+template <bool kFp8, int RW, int NB, int D>
+__device__ __forceinline__ void dot_steps(uint8_t* stage, __amdgpu_buffer_rsrc_t wr,
+                                          const uint32_t (&woff)[2], const int (&wrow)[2],
+                                          __amdgpu_buffer_rsrc_t xr, const uint32_t (&xoff)[NB],
+                                          __amdgpu_buffer_rsrc_t cr, uint32_t c0, uint32_t c1,
+                                          int s0, int n, int rot, f32x4 (&acc)[(NB + 1) / 2]) {
+  constexpr int kB = Step<kFp8>::kB, NTL = (NB + 1) / 2, RI = RW / 8;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int lr = lane >> 3, lc = lane & 7, i = lane & 15, g = lane >> 4;
+  v4u w[D][RI], x[D][NB][kB];
+  float a0[D], a1[D];
+  auto load = [&](int u, int q) __attribute__((always_inline)) {
+    const bool in = q < n;
+    int o = q + rot;
+    o = o >= n ? o - n : o;
+    const uint32_t s = (uint32_t)(s0 + o);
+#pragma unroll
+    for (int r = 0; r < RI; ++r) w[u][r] = load16_stream(wr, in ? woff[r] + s * 128 : kOutside);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int p = 0; p < kB; ++p)
+        x[u][b][p] = load16(xr, in && xoff[b] != kOutside
+                                    ? xoff[b] + s * (Step<kFp8>::kCols * 2) + 128 * p
+                                    : kOutside);
+    if constexpr (kFp8) {
+      a0[u] = load4(cr, in ? c0 + s * 4 : kOutside);
+      a1[u] = load4(cr, in ? c1 + s * 4 : kOutside);
+    }
+  };
+  uint8_t* xs = stage + 2048;
+  const int arow = RW == 8 ? i & 7 : i;  // rows 8-15 of an 8-row unit repeat: not used
+  auto compute = [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < RI; ++r) *reinterpret_cast<v4u*>(stage + tile_at(wrow[r], lc)) = w[u][r];
+    auto put_x = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        *reinterpret_cast<v4u*>(xs + tile_at(8 * b + lr, lc)) = x[u][b][p];
+      __builtin_amdgcn_wave_barrier();
+    };
+    put_x(0);
+    // a token tile's rows; with one group of 8 its rows twice (columns 8-15 unused)
+    auto trow = [&](int t) { return NB == 1 ? i & 7 : 16 * t + i; };
+    if constexpr (kFp8) {
+      f32x4 d[NTL];
+#pragma unroll
+      for (int t = 0; t < NTL; ++t) d[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (m > 0) put_x(m);
+        const v4u q = *reinterpret_cast<const v4u*>(stage + tile_at(arow, 4 * m + g));
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const bf16x8 a = widen8(q[2 * hh], q[2 * hh + 1]);
+#pragma unroll
+          for (int t = 0; t < NTL; ++t)
+            d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                a, *reinterpret_cast<const bf16x8*>(xs + tile_at(trow(t), 2 * g + hh)),
+                d[t], 0, 0, 0);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+#pragma unroll
+      for (int t = 0; t < NTL; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[t][r] = __builtin_fmaf(d[t][r], r < 2 ? a0[u] : a1[u], acc[t][r]);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(stage + tile_at(arow, 4 * m + g));
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a, *reinterpret_cast<const bf16x8*>(xs + tile_at(trow(t), 4 * m + g)), acc[t], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+#pragma unroll
+  for (int u = 0; u < D; ++u) load(u, u);
+  for (int q = 0; q < n; q += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      compute(u);
+      load(u, q + u + D);
+    }
+  }
+}
+
+// Gate/up: a unit is kUpCols intermediate columns of one live expert (8 gate and
+// 8 up rows) for kGroup of its picks, computed by KS waves, each a part of the K
+// steps (their sums are added in LDS in a fixed order); a block has kUpWaves /
+// KS units, or, of an expert with more picks, the same columns' units for all
+// its groups (the waves then read the same weights at one time). MFMA row i is gate row 2 (i / 4) + i % 4 for i % 4 < 2, else the up
+// row of the same column, so a lane's four results are g, g, u, u of two
+// neighbouring columns. kV > 0: the block routes all tokens itself (kV logits a
+// lane), block (0, 0) publishes; kV = 0: the plan is in the workspace. kMaxNB:
+// most eights of picks a unit can have.
+template <int kV, int KS, bool kFp8, int kMaxNB>
+__global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void layer_gate_up_kernel(
     const float* __restrict__ logits, const uint16_t* __restrict__ x, int T, int H, int E, int k,
-    int I, const uint8_t* __restrict__ w, const float* __restrict__ wsc,
+    int I, int G, const uint8_t* __restrict__ w, const float* __restrict__ wsc,
     int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, Plan plan,
     uint16_t* __restrict__ h) {
-  // a block that routes holds at most kRouteT tokens: one MFMA column group
-  constexpr int kMaxNT = kV > 0 ? 1 : 4;
+  static_assert(kV == 0 || kRouteT <= 8 * kMaxNB, "a routing block's picks fit one pass");
   __shared__ typename std::conditional<(kV > 0), PlanLds<32 * kRouteT>, int>::type P;
-  __shared__ f32x4 red[kUpWaves][kMaxNT][kWave];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[kUpWaves][stage_bytes(kMaxNB)];
+  __shared__ f32x4 red[KS > 1 ? kUpWaves : 1][(kMaxNB + 1) / 2][kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int slot = blockIdx.y;
   const int32_t* pick;
-  int e, first, cnt;
+  uint32_t word;
   if constexpr (kV > 0) {
-    route_and_plan<kWave * kUpWaves, kV>(P, logits, T, E, k, blockIdx.x == 0 && slot == 0,
-                                         topk_idx, topk_w, plan);
-    if (slot >= P.n) return;
-    e = P.expert[slot];
-    first = P.first[slot];
-    cnt = P.first[slot + 1] - first;
-    pick = P.pick + first;
+    route_and_plan<kWave * kUpWaves, kV>(P, logits, T, E, k, G, blockIdx.x == 0 && slot == 0,
+                                         topk_idx, topk_w, plan, gridDim.y);
+    word = slot < P.n ? P.slot[slot] : 0;
+    pick = P.pick;
   } else {
-    if (slot >= *plan.n) return;
-    e = plan.expert[slot];
-    first = plan.first[slot];
-    cnt = plan.first[slot + 1] - first;
-    pick = plan.pick + first;
+    word = plan.slot[slot];
+    pick = plan.pick;
   }
-  e = __builtin_amdgcn_readfirstlane(e);
-  cnt = __builtin_amdgcn_readfirstlane(cnt);
-  const int j0 = blockIdx.x * kUpCols;
-  const int i = lane & 15, g = lane >> 4;
-  const int row = (i & 3) < 2 ? j0 + 2 * (i >> 2) + (i & 3) : I + j0 + 2 * (i >> 2) + (i & 3) - 2;
-  const uint8_t* wp = w + ((int64_t)e * 2 * I + row) * H * (kFp8 ? 1 : 2) + 32 * g;
+  word = __builtin_amdgcn_readfirstlane(word);
+  const int e = slot_expert(word);
+  int cnt = slot_count(word);
+  if (cnt == 0) return;  // uniform over the block
+  const int ks = wid % KS;
+  // with parts (KS = 1 then): wave w takes group w % parts, the slot a share of the columns
+  const int parts = KS == 1 ? parts_of(cnt) : 1, grp = KS == 1 ? wid % parts : 0;
+  const int unit = KS == 1 ? (slot_part(word) * (int)gridDim.x + (int)blockIdx.x) * (kUpWaves / parts) +
+                                 wid / parts
+                           : (int)blockIdx.x * (kUpWaves / KS) + wid / KS;
+  pick += slot_first(word) + grp * kGroup;
+  cnt -= grp * kGroup;
+  if (KS == 1 && cnt <= 0) return;  // three groups of four
+  const int j0 = unit * kUpCols;
+  const int i = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
+  constexpr int kWB = kFp8 ? 1 : 2;  // bytes of a weight
+  const __amdgpu_buffer_rsrc_t wr =
+      make_rsrc(w + (int64_t)e * 2 * I * H * kWB, (int64_t)2 * I * H * kWB);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(x, (int64_t)T * H * 2);
+  const uint32_t woff[2] = {(uint32_t)(j0 + lr) * (uint32_t)(H * kWB) + 16 * lc,
+                            (uint32_t)(I + j0 + lr) * (uint32_t)(H * kWB) + 16 * lc};
+  const int wrow[2] = {4 * (lr >> 1) + (lr & 1), 4 * (lr >> 1) + (lr & 1) + 2};
   const int steps = H / Step<kFp8>::kCols;
-  const float *sc0 = nullptr, *sc1 = nullptr;
+  const int s0 = steps * ks / KS, n = steps * (ks + 1) / KS - s0;
+  const int rot = n > 0 ? (int)(blockIdx.x + slot) * 5 % n : 0;  // alike in a block: x from L1
+  __amdgpu_buffer_rsrc_t cr = xr;
+  uint32_t c0 = 0, c1 = 0;
   if constexpr (kFp8) {
-    sc0 = wsc + ((int64_t)e * (2 * I / kQuantBlock) + j0 / kQuantBlock) * steps;
-    sc1 = sc0 + (int64_t)(I / kQuantBlock) * steps;
+    const int nb = 2 * I / kQuantBlock;
+    cr = make_rsrc(wsc + (int64_t)e * nb * steps, (int64_t)nb * steps * 4);
+    c0 = (uint32_t)(j0 / kQuantBlock) * steps * 4;
+    c1 = c0 + (uint32_t)(I / kQuantBlock) * steps * 4;
   }
-  // up to 64 picks a pass over the weights
-  for (int c0 = 0; c0 < cnt; c0 += 64) {
-    auto pass = [&](auto nt_) __attribute__((always_inline)) {
-      constexpr int NT = decltype(nt_)::value;
-      const uint16_t* xp[NT];
-      f32x4 acc[NT];
+  auto pass = [&](auto nb_) __attribute__((always_inline)) {
+    constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
+    uint32_t xoff[NB];
+    f32x4 acc[NTL];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        // columns past the last pick repeat the first: never stored
-        const int c = c0 + 16 * nt + i;
-        xp[nt] = x + (int64_t)(pick[c < cnt ? c : 0] / k) * H + (Step<kFp8>::kCols / 4) * g;
-        acc[nt] = f32x4{0, 0, 0, 0};
-      }
-      dot_steps<kFp8, NT, NT == 1 ? 4 : (NT == 2 ? 2 : 1)>(wp, xp, sc0, sc1, wid, steps, kUpWaves,
-                                                          acc);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) red[wid][nt][lane] = acc[nt];
-      __syncthreads();
-      for (int nt = wid; nt < NT; nt += kUpWaves) {
-        f32x4 v = red[0][nt][lane];
-#pragma unroll
-        for (int q = 1; q < kUpWaves; ++q) v += red[q][nt][lane];
-        const int c = c0 + 16 * nt + i;
-        if (c < cnt) {
-          const uint32_t hv = bf16x2_rne(silu(v[0]) * v[2], silu(v[1]) * v[3]);
-          *reinterpret_cast<uint32_t*>(h + (int64_t)pick[c] * I + j0 + 2 * g) = hv;
-        }
-      }
-      __syncthreads();
-    };
-    const int left = cnt - c0;
-    if (kMaxNT == 1 || left <= 16) {
-      pass(std::integral_constant<int, 1>{});
-    } else if constexpr (kMaxNT > 1) {
-      if (left <= 32) pass(std::integral_constant<int, 2>{});
-      else pass(std::integral_constant<int, 4>{});
+    for (int b = 0; b < NB; ++b) {
+      const int c = 8 * b + lr;
+      xoff[b] = c < cnt ? (uint32_t)(pick[c] / k) * (uint32_t)(2 * H) + 16 * lc : kOutside;
     }
+#pragma unroll
+    for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    dot_steps<kFp8, 16, NB, kRing<kFp8, 16, NB>>(stage[wid], wr, woff, wrow, xr, xoff, cr, c0, c1, s0,
+                                             n, rot, acc);
+    if constexpr (KS > 1) {
+#pragma unroll
+      for (int t = 0; t < NTL; ++t) red[wid][t][lane] = acc[t];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int t = 0; t < NTL; ++t) {
+      if (KS > 1 && t % KS != ks) continue;  // uniform over the wave
+      f32x4 v = acc[t];
+      if constexpr (KS > 1) {
+        v = red[wid - ks][t][lane];
+#pragma unroll
+        for (int q = 1; q < KS; ++q) v += red[wid - ks + q][t][lane];
+      }
+      const int c = 16 * t + i;
+      if (c < cnt && (NB > 1 || i < 8)) {
+        const uint32_t hv = bf16x2_rne(silu(v[0]) * v[2], silu(v[1]) * v[3]);
+        *reinterpret_cast<uint32_t*>(h + (int64_t)pick[c] * I + j0 + 2 * g) = hv;
+      }
+    }
+  };
+  if (kMaxNB == 1 || cnt <= 8) {
+    pass(std::integral_constant<int, 1>{});
+  } else if constexpr (kMaxNB > 1) {
+    if (cnt <= 16) pass(std::integral_constant<int, 2>{});
+    else pass(std::integral_constant<int, 4>{});
   }
 }
 
 // Routing and plan alone (one block), where routing in every gate/up block
-// would cost more.
+// would cost more; V = 0: the plan of picks already made.
 template <int V>
 __global__ __launch_bounds__(1024) void layer_plan_kernel(const float* __restrict__ logits, int T,
-                                                          int E, int k,
+                                                          int E, int k, int G, int slots,
                                                           int32_t* __restrict__ topk_idx,
                                                           float* __restrict__ topk_w, Plan plan) {
   __shared__ PlanLds<kMaxPicks> P;
-  route_and_plan<1024, V>(P, logits, T, E, k, true, topk_idx, topk_w, plan);
+  route_and_plan<1024, V>(P, logits, T, E, k, G, true, topk_idx, topk_w, plan, slots);
 }
 
-// Down and combine: a block computes kDownCols columns of y for all tokens. The
-// K steps of all live experts in a row are cut into one range a wave; at the
-// end of an expert's part of its range a wave adds gate weight x result to its
-// own fp32 rows of y in LDS (an expert's picks are different tokens), and the
-// waves' rows are added in a fixed order at the end.
-template <bool kFp8>
-__global__ __launch_bounds__(kWave * kDownWaves) void layer_down_kernel(
-    const uint16_t* __restrict__ h, int T, int H, int k, int I, const uint8_t* __restrict__ w,
-    const float* __restrict__ wsc, const float* __restrict__ topk_w, Plan plan,
-    uint16_t* __restrict__ y) {
-  extern __shared__ __attribute__((aligned(16))) float ya[];  // [kDownWaves][T][kDownCols]
+// Down and combine: a block computes RW columns of y for all tokens. The K steps
+// of all slots in a row are cut into one range a wave; at the end of an
+// expert's part of its range a wave adds gate weight x result to its own fp32
+// rows of y in LDS (an expert's picks are different tokens), and the waves' rows
+// are added in a fixed order at the end.
+template <bool kFp8, int RW, int kMaxNB, int DW>
+__global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
+    const uint16_t* __restrict__ h, int T, int H, int k, int I, int slots,
+    const uint8_t* __restrict__ w, const float* __restrict__ wsc,
+    const float* __restrict__ topk_w, Plan plan, uint16_t* __restrict__ y) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int np = T * k;
+  uint8_t* stage = lds;                                       // [DW][stage_bytes]
+  float* ya = reinterpret_cast<float*>(lds + DW * stage_bytes(kMaxNB));
+  float* gw = ya + (size_t)DW * T * RW;               // [np], ya: [DW][T][RW]
+  uint32_t* sl = reinterpret_cast<uint32_t*>(gw + np);        // [slots]
+  uint16_t* pk = reinterpret_cast<uint16_t*>(sl + slots);     // [np]
+  constexpr int NT = kWave * DW;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int c0 = blockIdx.x * kDownCols;
-  for (int q = tid; q < kDownWaves * T * kDownCols; q += kWave * kDownWaves) ya[q] = 0.f;
-  __syncthreads();
+  const int c0 = blockIdx.x * RW;
   const int n = *plan.n;
+  for (int p = tid; p < np; p += NT) {
+    gw[p] = topk_w[p];
+    pk[p] = (uint16_t)plan.pick[p];
+  }
+  for (int s = tid; s < slots; s += NT) sl[s] = plan.slot[s];
+  for (int q = tid; q < DW * T * RW; q += NT) ya[q] = 0.f;
+  __syncthreads();
   const int steps = I / Step<kFp8>::kCols;
-  const int total = n * steps;
-  int at = (int)((int64_t)total * wid / kDownWaves);
-  const int end = (int)((int64_t)total * (wid + 1) / kDownWaves);
-  const int i = lane & 15, g = lane >> 4;
-  float* mine = ya + (size_t)wid * T * kDownCols;
+  const int64_t total = (int64_t)n * steps;
+  int at = (int)(total * wid / DW);
+  const int end = (int)(total * (wid + 1) / DW);
+  const int i = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
+  float* mine = ya + (size_t)wid * T * RW;
+  constexpr int kWB = kFp8 ? 1 : 2;
+  const __amdgpu_buffer_rsrc_t hr = make_rsrc(h, (int64_t)np * I * 2);
+  const uint32_t woff[2] = {(uint32_t)(c0 + lr) * (uint32_t)(I * kWB) + 16 * lc,
+                            (uint32_t)(c0 + 8 + lr) * (uint32_t)(I * kWB) + 16 * lc};
+  const int wrow[2] = {lr, 8 + lr};
   while (at < end) {
     const int slot = at / steps;
     const int s0 = at - slot * steps;
     const int s1 = end - at < steps - s0 ? s0 + (end - at) : steps;
     at += s1 - s0;
-    const int e = __builtin_amdgcn_readfirstlane(plan.expert[slot]);
-    const int first = __builtin_amdgcn_readfirstlane(plan.first[slot]);
-    const int cnt = __builtin_amdgcn_readfirstlane(plan.first[slot + 1]) - first;
-    const int32_t* pick = plan.pick + first;
-    const uint8_t* wp = w + ((int64_t)e * H + c0 + i) * I * (kFp8 ? 1 : 2) + 32 * g;
-    const float* sc = nullptr;
-    if constexpr (kFp8)
-      sc = wsc + ((int64_t)e * (H / kQuantBlock) + c0 / kQuantBlock) * steps;
-    for (int b0 = 0; b0 < cnt; b0 += 64) {
-      auto pass = [&](auto nt_) __attribute__((always_inline)) {
-        constexpr int NT = decltype(nt_)::value;
-        const uint16_t* hp[NT];
-        f32x4 acc[NT];
+    const int rot = blockIdx.x * 5 % (s1 - s0);
+    const uint32_t word = __builtin_amdgcn_readfirstlane(sl[slot]);
+    const int e = slot_expert(word), grp = slot_part(word);
+    const int cnt = slot_count(word) - grp * kGroup;  // this part's picks (and further ones)
+    if (cnt <= 0) continue;                           // three groups of four
+    const uint16_t* pick = pk + slot_first(word) + grp * kGroup;
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(w + (int64_t)e * H * I * kWB, (int64_t)H * I * kWB);
+    __amdgpu_buffer_rsrc_t cr = hr;
+    uint32_t sc = 0;
+    if constexpr (kFp8) {
+      const int nb = H / kQuantBlock;
+      cr = make_rsrc(wsc + (int64_t)e * nb * steps, (int64_t)nb * steps * 4);
+      sc = (uint32_t)(c0 / kQuantBlock) * steps * 4;
+    }
+    auto pass = [&](auto nb_) __attribute__((always_inline)) {
+      constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
+      uint32_t hoff[NB];
+      f32x4 acc[NTL];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int c = b0 + 16 * nt + i;
-          hp[nt] = h + (int64_t)pick[c < cnt ? c : 0] * I + (Step<kFp8>::kCols / 4) * g;
-          acc[nt] = f32x4{0, 0, 0, 0};
+      for (int b = 0; b < NB; ++b) {
+        const int c = 8 * b + lr;
+        hoff[b] = c < cnt ? (uint32_t)pick[c] * (uint32_t)(2 * I) + 16 * lc : kOutside;
+      }
+#pragma unroll
+      for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
+      dot_steps<kFp8, RW, NB, kRing<kFp8, RW, NB>>(stage + wid * stage_bytes(kMaxNB), wr, woff, wrow,
+                                                hr, hoff, cr, sc, sc, s0, s1 - s0, rot, acc);
+#pragma unroll
+      for (int t = 0; t < NTL; ++t) {
+        const int c = 16 * t + i;
+        if (c < cnt && (NB > 1 || i < 8) && (RW == 16 || g < 2)) {
+          const int p = pick[c];
+          const float gp = gw[p];
+          f32x4* dst = reinterpret_cast<f32x4*>(mine + (p / k) * RW + 4 * g);
+          f32x4 v = *dst;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gp, acc[t][r], v[r]);
+          *dst = v;
         }
-        dot_steps<kFp8, NT, NT == 1 ? 4 : (NT == 2 ? 2 : 1)>(wp, hp, sc, sc, s0, s1, 1, acc);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int c = b0 + 16 * nt + i;
-          if (c < cnt) {
-            const int p = pick[c];
-            const float gw = topk_w[p];
-            f32x4* dst = reinterpret_cast<f32x4*>(mine + (p / k) * kDownCols + 4 * g);
-            f32x4 v = *dst;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gw, acc[nt][r], v[r]);
-            *dst = v;
-          }
-        }
-      };
-      const int left = cnt - b0;
-      if (left <= 16) pass(std::integral_constant<int, 1>{});
-      else if (left <= 32) pass(std::integral_constant<int, 2>{});
+      }
+    };
+    if (kMaxNB == 1 || cnt <= 8) {
+      pass(std::integral_constant<int, 1>{});
+    } else if constexpr (kMaxNB > 1) {
+      if (cnt <= 16) pass(std::integral_constant<int, 2>{});
       else pass(std::integral_constant<int, 4>{});
     }
   }
   __syncthreads();
-  for (int q = tid; q < T * kDownCols / 2; q += kWave * kDownWaves) {
-    const int t = q / (kDownCols / 2), c = (q - t * (kDownCols / 2)) * 2;
-    float a = 0.f, b = 0.f;
+  for (int q = tid; q < T * RW / 2; q += NT) {
+    const int t = q / (RW / 2), c = (q - t * (RW / 2)) * 2;
+    float2 a = {0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < kDownWaves; ++v) {
-      const float2 u = *reinterpret_cast<const float2*>(ya + ((size_t)v * T + t) * kDownCols + c);
-      a += u.x;
-      b += u.y;
+    for (int v = 0; v < DW; ++v) {
+      const float2 u = *reinterpret_cast<const float2*>(ya + ((size_t)v * T + t) * RW + c);
+      a.x += u.x;
+      a.y += u.y;
     }
-    *reinterpret_cast<uint32_t*>(y + (int64_t)t * H + c0 + c) = bf16x2_rne(a, b);
+    *reinterpret_cast<uint32_t*>(y + (int64_t)t * H + c0 + c) = bf16x2_rne(a.x, a.y);
   }
+}
+
+// Lanes a token (a power of two >= k): as few as leave at most V logits a lane.
+int route_lanes(int E, int k, int V) {
+  int G = 1;
+  while (G < kWave && (G < k || G * V < E)) G <<= 1;
+  return G;
 }
 
 }  // namespace
 
 int64_t layer_plan_ints(int T, int E, int k) {
-  const int np = T * k, slots = np < E ? np : E;
-  return 4 + 2 * (int64_t)slots + 1 + np;
+  return 4 + (int64_t)max_slots(E, T * k) + T * k;
 }
+
+namespace {
+
+template <bool kFp8>
+hipError_t run_layer(const float* logits, const void* x, int T, int H, int E, int k, int I,
+                     const void* w_gate_up, const float* s_gate_up, const void* w_down,
+                     const float* s_down, int32_t* topk_idx, float* topk_w, void* h,
+                     int32_t* plan_ws, void* y, hipStream_t s) {
+  const int np = T * k;
+  const int slots = T > kGroup ? max_slots(E, np) : (np < E ? np : E);  // no parts with few tokens
+  const Plan plan = plan_at(plan_ws, slots);
+  auto up = [&](auto kernel, int KS, int G) {
+    return launch(kernel, dim3((unsigned)(I / kUpCols * KS / kUpWaves), (unsigned)slots),
+                  dim3(kWave * kUpWaves), 0, s, logits, static_cast<const uint16_t*>(x), T, H, E, k,
+                  I, G, static_cast<const uint8_t*>(w_gate_up), s_gate_up, topk_idx, topk_w, plan,
+                  static_cast<uint16_t*>(h));
+  };
+  hipError_t err;
+  if (T <= kRouteT) {
+    // two waves a unit while that is what fills the chip (16 waves a compute
+    // unit): T = 1 up launch 36 us against 41 with four; T = 8 with 8-bit weights
+    // 101 us with one against 119 with two
+    const int G4 = route_lanes(E, k, 4), G16 = route_lanes(E, k, 16);
+    if (slots * (I / kUpCols) >= 4096)
+      err = E <= 256 ? up(layer_gate_up_kernel<4, 1, kFp8, 1>, 1, G4)
+                     : up(layer_gate_up_kernel<16, 1, kFp8, 1>, 1, G16);
+    else
+      err = E <= 256 ? up(layer_gate_up_kernel<4, 2, kFp8, 1>, 2, G4)
+                     : up(layer_gate_up_kernel<16, 2, kFp8, 1>, 2, G16);
+  } else {
+    auto go = [&](auto kernel, int V) {
+      return launch(kernel, dim3(1), dim3(1024), 0, s, logits, T, E, k, route_lanes(E, k, V), slots,
+                    topk_idx, topk_w, plan);
+    };
+    // one block routes as many tokens as it can take at a time; more of them
+    // are routed by a launch of their own (T = 128, E = 128, k = 8: 19 us for both
+    // in one block)
+    if (T * route_lanes(E, k, 4) <= 1024 && E <= 256) {
+      err = go(layer_plan_kernel<4>, 4);
+    } else {
+      err = launch_route(logits, T, E, k, topk_idx, topk_w, s);
+      if (err != hipSuccess) return err;
+      err = go(layer_plan_kernel<0>, 4);
+    }
+    if (err != hipSuccess) return err;
+    err = up(layer_gate_up_kernel<0, 1, kFp8, 4>, 1, 0);
+  }
+  if (err != hipSuccess) return err;
+  auto lds = [&](int RW, int NB, int DW) {
+    return (uint32_t)(DW * (stage_bytes(NB) + T * RW * 4) + np * 4 + slots * 4 + np * 2);
+  };
+  auto down = [&](auto rw, auto nb, auto dw) {
+    constexpr int RW = decltype(rw)::value, NB = decltype(nb)::value, DW = decltype(dw)::value;
+    return launch(layer_down_kernel<kFp8, RW, NB, DW>, dim3((unsigned)(H / RW)), dim3(kWave * DW),
+                  lds(RW, NB, DW), s, static_cast<const uint16_t*>(h), T, H, k, I, slots,
+                  static_cast<const uint8_t*>(w_down), s_down, topk_w, plan,
+                  static_cast<uint16_t*>(y));
+  };
+  auto columns = [&](auto rw) {
+    using I1 = std::integral_constant<int, 1>;
+    using I4 = std::integral_constant<int, 4>;
+    using I8 = std::integral_constant<int, 8>;
+    using I16 = std::integral_constant<int, 16>;
+    if (T <= 8) return down(rw, I1{}, I16{});
+    return down(rw, I4{}, I8{});
+  };
+  // 16 columns a block where that makes a block for every compute unit
+  return H / 16 >= 256 ? columns(std::integral_constant<int, 16>{})
+                       : columns(std::integral_constant<int, 8>{});
+}
+
+}  // namespace
 
 hipError_t launch_layer(const float* logits, const void* x, int T, int H, int E, int k, int I,
                         bool fp8, const void* w_gate_up, const float* s_gate_up,
                         const void* w_down, const float* s_down, int32_t* topk_idx, float* topk_w,
                         void* h, int32_t* plan_ws, void* y, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const int np = T * k, slots = np < E ? np : E;
-  const Plan plan = plan_at(plan_ws, slots);
-  const dim3 grid((unsigned)(I / kUpCols), (unsigned)slots), block(kWave * kUpWaves);
-  auto up = [&](auto kernel) {
-    return launch(kernel, grid, block, 0, s, logits, static_cast<const uint16_t*>(x), T, H, E, k, I,
-                  static_cast<const uint8_t*>(w_gate_up), s_gate_up, topk_idx, topk_w, plan,
-                  static_cast<uint16_t*>(h));
-  };
-  hipError_t err;
-  if (T <= kRouteT) {
-    err = E <= 256 ? (fp8 ? up(layer_gate_up_kernel<4, true>) : up(layer_gate_up_kernel<4, false>))
-                   : (fp8 ? up(layer_gate_up_kernel<16, true>) : up(layer_gate_up_kernel<16, false>));
-  } else {
-    auto go = [&](auto kernel) {
-      return launch(kernel, dim3(1), dim3(1024), 0, s, logits, T, E, k, topk_idx, topk_w, plan);
-    };
-    err = E <= 256 ? go(layer_plan_kernel<4>) : go(layer_plan_kernel<16>);
-    if (err != hipSuccess) return err;
-    err = fp8 ? up(layer_gate_up_kernel<0, true>) : up(layer_gate_up_kernel<0, false>);
-  }
-  if (err != hipSuccess) return err;
-  const dim3 dgrid((unsigned)(H / kDownCols)), dblock(kWave * kDownWaves);
-  const uint32_t lds = (uint32_t)(kDownWaves * T * kDownCols * 4);
-  auto down = [&](auto kernel) {
-    return launch(kernel, dgrid, dblock, lds, s, static_cast<const uint16_t*>(h), T, H, k, I,
-                  static_cast<const uint8_t*>(w_down), s_down, topk_w, plan,
-                  static_cast<uint16_t*>(y));
-  };
-  return fp8 ? down(layer_down_kernel<true>) : down(layer_down_kernel<false>);
+  return fp8 ? run_layer<true>(logits, x, T, H, E, k, I, w_gate_up, s_gate_up, w_down, s_down,
+                               topk_idx, topk_w, h, plan_ws, y, s)
+             : run_layer<false>(logits, x, T, H, E, k, I, w_gate_up, s_gate_up, w_down, s_down,
+                                topk_idx, topk_w, h, plan_ws, y, s);
 }
 
 }  // namespace moe
