@@ -231,6 +231,12 @@ hipError_t launch_dispatch_fp8(const void* x, int dtype, const int32_t* pos, int
 hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
                            const int32_t* offs, const int32_t* cnts, const void* w,
                            const float* wsc, int N, int K, void* out, hipStream_t s);
+// The same (gate_up: with the FFN's epilogue, c = hq, csc = hs, N = 2 I) for few
+// rows an expert: weights streamed, tiles of 32 rows.
+hipError_t launch_gemm_fp8_stream(bool gate_up, const void* a, const float* asc, int64_t rows,
+                                  int E, const int32_t* offs, const int32_t* cnts, const void* w,
+                                  const float* wsc, int N, int K, void* c, float* csc,
+                                  hipStream_t s);
 // The SwiGLU FFN on 8-bit rows: gate/up product with SiLU, u and the row
 // quantisation of h fused into hq [rows][I] and hs [rows][I/128], then the down
 // product. H % 128 == 0, I % 128 == 0.

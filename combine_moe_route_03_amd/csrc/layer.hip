@@ -23,12 +23,12 @@
 #include "launch.h"
 #include "quant.h"
 #include "route_token.h"
+#include "stream.h"
 
 namespace moe {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxPicks = 1024;
 constexpr int kMaxE = 1024;
@@ -163,38 +163,12 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {
   return bf16x8{w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
 }
 
-// ---- the weight stream. A unit is 16 (or 8) weight rows; a K step is 128 bytes
-// of each: 64 bf16 or 128 e4m3 columns. Every load instruction takes whole
-// 128-byte lines, lane l chunk l % 8 of row l / 8 (16 bytes a lane): lanes in
-// the order of an MFMA operand, 16 rows by 64 bytes, reached 5.6-6.2 TB/s on the
-// same stream, this order 6.9-7.0. The loads of D steps are in flight in
-// a register ring; a step's registers then go through the wave's own piece of
-// LDS into operand order (no barrier: a wave's LDS operations are in order).
-// Units start at different steps, since weight rows a power of two apart would
-// otherwise have all waves on the same memory channels at one time (5.9 against
-// 6.2-7.0 TB/s).
+// K steps of the weight stream (stream.h): 64 bf16 or 128 e4m3 columns.
 template <bool kFp8>
 struct Step {
   static constexpr int kCols = kFp8 ? 128 : 64;
   static constexpr int kB = kFp8 ? 2 : 1;  // 128-byte pieces of a token row a step
 };
-
-constexpr uint32_t kOutside = 0xFFFFFFF0u;  // byte offset outside every descriptor's range
-constexpr int kStream = 2;                  // cache policy: weights are read once
-
-__device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
-}
-__device__ __forceinline__ v4u load16_stream(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStream);
-}
-__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
-
-// Byte offset of 16-byte chunk c of LDS tile row r (rows of 128 bytes): the 16
-// lanes that read one chunk column at a time hit distinct banks.
-__device__ __forceinline__ int tile_at(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
 
 // Bytes of LDS a wave needs for NB groups of 8 tokens, and the steps in flight
 // that fit 168 registers (three waves a SIMD).
@@ -204,16 +178,15 @@ constexpr int kRing = kFp8 ? (NB == 1 ? (RW == 8 ? 6 : 4) : (NB == 2 ? 3 : 2))
                            : (NB == 1 ? (RW == 8 ? 8 : 6) : (NB == 2 ? 4 : 3));
 
 // acc[t] += the products of the unit's rows with NB x 8 tokens over n K steps
-// from s0, beginning with step s0 + rot. woff: byte offsets in wr of the lane's two rows at
-// its chunk (RW = 8: the first only), wrow their LDS rows; xoff[b]: in xr of
-// its token of group b at its chunk (kOutside without a token: zeros, no memory
-// access); c0, c1 (e4m3): in cr of the scales of D registers 0-1 and 2-3, one a
-// step. Steps past the last are outside the range, so the loop has no branches.
+// from s0, beginning with step s0 + rot. woff: byte offsets in wb of the lane's two rows at
+// its chunk (RW = 8: the first only), wrow their LDS rows; xoff[b]: in xb of
+// its token of group b at its chunk (kOutside without a token); c0, c1 (e4m3): in cb of the scales of D registers 0-1 and 2-3, one a
+// step.
 template <bool kFp8, int RW, int NB, int D>
-__device__ __forceinline__ void dot_steps(uint8_t* stage, __amdgpu_buffer_rsrc_t wr,
+__device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
                                           const uint32_t (&woff)[2], const int (&wrow)[2],
-                                          __amdgpu_buffer_rsrc_t xr, const uint32_t (&xoff)[NB],
-                                          __amdgpu_buffer_rsrc_t cr, uint32_t c0, uint32_t c1,
+                                          const Buffer& xb, const uint32_t (&xoff)[NB],
+                                          const Buffer& cb, uint32_t c0, uint32_t c1,
                                           int s0, int n, int rot, f32x4 (&acc)[(NB + 1) / 2]) {
   constexpr int kB = Step<kFp8>::kB, NTL = (NB + 1) / 2, RI = RW / 8;
   const int lane = threadIdx.x & (kWave - 1);
@@ -224,19 +197,17 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, __amdgpu_buffer_rsrc_t
     const bool in = q < n;
     int o = q + rot;
     o = o >= n ? o - n : o;
-    const uint32_t s = (uint32_t)(s0 + o);
+    const uint32_t s = in ? (uint32_t)(s0 + o) : 0;
 #pragma unroll
-    for (int r = 0; r < RI; ++r) w[u][r] = load16_stream(wr, in ? woff[r] + s * 128 : kOutside);
+    for (int r = 0; r < RI; ++r) w[u][r] = load16_stream(wb.at(in), woff[r], s * 128);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int p = 0; p < kB; ++p)
-        x[u][b][p] = load16(xr, in && xoff[b] != kOutside
-                                    ? xoff[b] + s * (Step<kFp8>::kCols * 2) + 128 * p
-                                    : kOutside);
+        x[u][b][p] = load16(xb.at(in), xoff[b], s * (Step<kFp8>::kCols * 2) + 128 * p);
     if constexpr (kFp8) {
-      a0[u] = load4(cr, in ? c0 + s * 4 : kOutside);
-      a1[u] = load4(cr, in ? c1 + s * 4 : kOutside);
+      a0[u] = load4(cb.at(in), c0, s * 4);
+      a1[u] = load4(cb.at(in), c1, s * 4);
     }
   };
   uint8_t* xs = stage + 2048;
@@ -349,20 +320,19 @@ __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void 
   const int j0 = unit * kUpCols;
   const int i = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
   constexpr int kWB = kFp8 ? 1 : 2;  // bytes of a weight
-  const __amdgpu_buffer_rsrc_t wr =
-      make_rsrc(w + (int64_t)e * 2 * I * H * kWB, (int64_t)2 * I * H * kWB);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(x, (int64_t)T * H * 2);
+  const Buffer wb = {w + (int64_t)e * 2 * I * H * kWB, (uint32_t)(2 * I) * (uint32_t)(H * kWB)};
+  const Buffer xb = {x, (uint32_t)T * (uint32_t)(2 * H)};
   const uint32_t woff[2] = {(uint32_t)(j0 + lr) * (uint32_t)(H * kWB) + 16 * lc,
                             (uint32_t)(I + j0 + lr) * (uint32_t)(H * kWB) + 16 * lc};
   const int wrow[2] = {4 * (lr >> 1) + (lr & 1), 4 * (lr >> 1) + (lr & 1) + 2};
   const int steps = H / Step<kFp8>::kCols;
   const int s0 = steps * ks / KS, n = steps * (ks + 1) / KS - s0;
   const int rot = n > 0 ? (int)(blockIdx.x + slot) * 5 % n : 0;  // alike in a block: x from L1
-  __amdgpu_buffer_rsrc_t cr = xr;
+  Buffer cb = xb;
   uint32_t c0 = 0, c1 = 0;
   if constexpr (kFp8) {
     const int nb = 2 * I / kQuantBlock;
-    cr = make_rsrc(wsc + (int64_t)e * nb * steps, (int64_t)nb * steps * 4);
+    cb = {wsc + (int64_t)e * nb * steps, (uint32_t)nb * steps * 4};
     c0 = (uint32_t)(j0 / kQuantBlock) * steps * 4;
     c1 = c0 + (uint32_t)(I / kQuantBlock) * steps * 4;
   }
@@ -377,7 +347,7 @@ __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void 
     }
 #pragma unroll
     for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
-    dot_steps<kFp8, 16, NB, kRing<kFp8, 16, NB>>(stage[wid], wr, woff, wrow, xr, xoff, cr, c0, c1, s0,
+    dot_steps<kFp8, 16, NB, kRing<kFp8, 16, NB>>(stage[wid], wb, woff, wrow, xb, xoff, cb, c0, c1, s0,
                                              n, rot, acc);
     if constexpr (KS > 1) {
 #pragma unroll
@@ -455,7 +425,7 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
   const int i = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
   float* mine = ya + (size_t)wid * T * RW;
   constexpr int kWB = kFp8 ? 1 : 2;
-  const __amdgpu_buffer_rsrc_t hr = make_rsrc(h, (int64_t)np * I * 2);
+  const Buffer hb = {h, (uint32_t)np * (uint32_t)(2 * I)};
   const uint32_t woff[2] = {(uint32_t)(c0 + lr) * (uint32_t)(I * kWB) + 16 * lc,
                             (uint32_t)(c0 + 8 + lr) * (uint32_t)(I * kWB) + 16 * lc};
   const int wrow[2] = {lr, 8 + lr};
@@ -470,12 +440,12 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
     const int cnt = slot_count(word) - grp * kGroup;  // this part's picks (and further ones)
     if (cnt <= 0) continue;                           // three groups of four
     const uint16_t* pick = pk + slot_first(word) + grp * kGroup;
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc(w + (int64_t)e * H * I * kWB, (int64_t)H * I * kWB);
-    __amdgpu_buffer_rsrc_t cr = hr;
+    const Buffer wb = {w + (int64_t)e * H * I * kWB, (uint32_t)H * (uint32_t)(I * kWB)};
+    Buffer cb = hb;
     uint32_t sc = 0;
     if constexpr (kFp8) {
       const int nb = H / kQuantBlock;
-      cr = make_rsrc(wsc + (int64_t)e * nb * steps, (int64_t)nb * steps * 4);
+      cb = {wsc + (int64_t)e * nb * steps, (uint32_t)nb * steps * 4};
       sc = (uint32_t)(c0 / kQuantBlock) * steps * 4;
     }
     auto pass = [&](auto nb_) __attribute__((always_inline)) {
@@ -489,8 +459,8 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
       }
 #pragma unroll
       for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
-      dot_steps<kFp8, RW, NB, kRing<kFp8, RW, NB>>(stage + wid * stage_bytes(kMaxNB), wr, woff, wrow,
-                                                hr, hoff, cr, sc, sc, s0, s1 - s0, rot, acc);
+      dot_steps<kFp8, RW, NB, kRing<kFp8, RW, NB>>(stage + wid * stage_bytes(kMaxNB), wb, woff, wrow,
+                                                hb, hoff, cb, sc, sc, s0, s1 - s0, rot, acc);
 #pragma unroll
       for (int t = 0; t < NTL; ++t) {
         const int c = 16 * t + i;
