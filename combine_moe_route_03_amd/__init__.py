@@ -658,21 +658,26 @@ def combine(expert_out: torch.Tensor, topk_w: torch.Tensor, pos: torch.Tensor, s
 _FP8 = torch.float8_e4m3fn
 
 
-def _checked(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> int:
-    """Address of a contiguous tensor of this shape and type on the current device."""
-    if t.dtype != dtype:
+def _checked(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype,
+             device: torch.device) -> int:
+    """Address of a contiguous tensor of this shape and type on this device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to libmoe_route must be contiguous")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current device, got {t.device}")
-    return t.data_ptr()
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError("tensors passed to libmoe_route must be contiguous")
 
 
-def _current_stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _current_stream(device: torch.device) -> int:
+    """The current stream of the current device, which `device` has to be (the
+    raw handle: a Stream object costs 2-3 us, as much as the smallest kernel)."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current device, got {device}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _blocks(n: int) -> int:
@@ -688,18 +693,19 @@ def quantize(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None = None
         raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
     if x.dim() < 2 or block_rows not in (1, 128):
         raise ValueError("x needs at least two dimensions, block_rows must be 1 or 128")
+    dev = x.device
     shape = tuple(x.shape)
     lead, rows, cols = shape[:-2], shape[-2], shape[-1]
     batch = 1
     for n in lead:
         batch *= n
     sshape = (*lead, -(-rows // block_rows), _blocks(cols))
-    q = _empty(shape, _FP8, x.device) if q is None else q
-    scale = _empty(sshape, torch.float32, x.device) if scale is None else scale
+    q = _empty(shape, _FP8, dev) if q is None else q
+    scale = _empty(sshape, torch.float32, dev) if scale is None else scale
     _check(lib().moe_quantize(
-        _checked("x", x, shape, x.dtype), _DTYPE_CODE[x.dtype], batch, rows, cols, block_rows,
-        _checked("q", q, shape, _FP8), _checked("scale", scale, sshape, torch.float32),
-        _current_stream()), "moe_quantize")
+        _checked("x", x, shape, x.dtype, dev), _DTYPE_CODE[x.dtype], batch, rows, cols, block_rows,
+        _checked("q", q, shape, _FP8, dev), _checked("scale", scale, sshape, torch.float32, dev),
+        _current_stream(dev)), "moe_quantize")
     return q, scale
 
 
@@ -709,13 +715,14 @@ def dispatch_copy_fp8(x: torch.Tensor, pos: torch.Tensor, shape: Shape,
     """The dispatch copy with the rows quantised on the way: (send_q
     float8_e4m3fn [T*k, H], send_scale float32 [T*k, ceil(H/128)])."""
     T, H, k = shape.T, shape.H, shape.k
+    dev = x.device
     qs, ss = (T * k, H), (T * k, _blocks(H))
-    send_q = _empty(qs, _FP8, x.device) if send_q is None else send_q
-    send_scale = _empty(ss, torch.float32, x.device) if send_scale is None else send_scale
+    send_q = _empty(qs, _FP8, dev) if send_q is None else send_q
+    send_scale = _empty(ss, torch.float32, dev) if send_scale is None else send_scale
     _check(lib().moe_dispatch_copy_fp8(
-        ctypes.byref(shape.c()), _checked("x", x, (T, H), shape.dtype),
-        _checked("pos", pos, (T, k), torch.int32), _checked("send_q", send_q, qs, _FP8),
-        _checked("send_scale", send_scale, ss, torch.float32), _current_stream()),
+        ctypes.byref(shape.c()), _checked("x", x, (T, H), shape.dtype, dev),
+        _checked("pos", pos, (T, k), torch.int32, dev), _checked("send_q", send_q, qs, _FP8, dev),
+        _checked("send_scale", send_scale, ss, torch.float32, dev), _current_stream(dev)),
         "moe_dispatch_copy_fp8")
     return send_q, send_scale
 
@@ -727,17 +734,18 @@ def expert_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: torc
     with block scales, into bfloat16 [rows, N]."""
     if a.dim() != 2 or w.dim() != 3:
         raise ValueError("a must be [rows, K] and w [E, N, K]")
+    dev = a.device
     rows, K = a.shape
     E, N, _ = w.shape
-    out = _empty((rows, N), torch.bfloat16, a.device) if out is None else out
+    out = _empty((rows, N), torch.bfloat16, dev) if out is None else out
     f32, i32 = torch.float32, torch.int32
     _check(lib().moe_expert_gemm_fp8(
-        rows, E, N, K, _checked("a", a, (rows, K), _FP8),
-        _checked("a_scale", a_scale, (rows, _blocks(K)), f32),
-        _checked("expert_offsets", expert_offsets, (E,), i32),
-        _checked("expert_counts", expert_counts, (E,), i32), _checked("w", w, (E, N, K), _FP8),
-        _checked("w_scale", w_scale, (E, _blocks(N), _blocks(K)), f32),
-        _checked("out", out, (rows, N), torch.bfloat16), _current_stream()),
+        rows, E, N, K, _checked("a", a, (rows, K), _FP8, dev),
+        _checked("a_scale", a_scale, (rows, _blocks(K)), f32, dev),
+        _checked("expert_offsets", expert_offsets, (E,), i32, dev),
+        _checked("expert_counts", expert_counts, (E,), i32, dev), _checked("w", w, (E, N, K), _FP8, dev),
+        _checked("w_scale", w_scale, (E, _blocks(N), _blocks(K)), f32, dev),
+        _checked("out", out, (rows, N), torch.bfloat16, dev), _current_stream(dev)),
         "moe_expert_gemm_fp8")
     return out
 
@@ -760,24 +768,25 @@ def expert_swiglu_fp8(send_q: torch.Tensor, send_scale: torch.Tensor,
     """SwiGLU expert FFN on 8-bit rows and weights (w_gate_up [E, 2I, H], w_down
     [E, H, I] float8_e4m3fn with 128 x 128 block scales) into bfloat16 [T*k, H].
     shape.dtype is the output's: bfloat16."""
+    dev = send_q.device
     E, H, rows = shape.E, shape.H, shape.T * shape.k
     I = w_down.shape[-1]
     f32, i32 = torch.float32, torch.int32
-    expert_out = _empty((rows, H), torch.bfloat16, send_q.device) if expert_out is None \
+    expert_out = _empty((rows, H), torch.bfloat16, dev) if expert_out is None \
         else expert_out
-    workspace = _workspace(workspace, expert_swiglu_fp8_workspace_bytes(shape, I), send_q.device)
+    workspace = _workspace(workspace, expert_swiglu_fp8_workspace_bytes(shape, I), dev)
     _check(lib().moe_expert_swiglu_fp8(
-        ctypes.byref(shape.c()), I, _checked("send_q", send_q, (rows, H), _FP8),
-        _checked("send_scale", send_scale, (rows, _blocks(H)), f32),
-        _checked("expert_offsets", expert_offsets, (E,), i32),
-        _checked("expert_counts", expert_counts, (E,), i32),
-        _checked("w_gate_up", w_gate_up, (E, 2 * I, H), _FP8),
-        _checked("s_gate_up", s_gate_up, (E, _blocks(2 * I), _blocks(H)), f32),
-        _checked("w_down", w_down, (E, H, I), _FP8),
-        _checked("s_down", s_down, (E, _blocks(H), _blocks(I)), f32),
-        _checked("expert_out", expert_out, (rows, H), torch.bfloat16),
-        _checked("workspace", workspace, tuple(workspace.shape), torch.uint8), workspace.numel(),
-        _current_stream()), "moe_expert_swiglu_fp8")
+        ctypes.byref(shape.c()), I, _checked("send_q", send_q, (rows, H), _FP8, dev),
+        _checked("send_scale", send_scale, (rows, _blocks(H)), f32, dev),
+        _checked("expert_offsets", expert_offsets, (E,), i32, dev),
+        _checked("expert_counts", expert_counts, (E,), i32, dev),
+        _checked("w_gate_up", w_gate_up, (E, 2 * I, H), _FP8, dev),
+        _checked("s_gate_up", s_gate_up, (E, _blocks(2 * I), _blocks(H)), f32, dev),
+        _checked("w_down", w_down, (E, H, I), _FP8, dev),
+        _checked("s_down", s_down, (E, _blocks(H), _blocks(I)), f32, dev),
+        _checked("expert_out", expert_out, (rows, H), torch.bfloat16, dev),
+        _checked("workspace", workspace, tuple(workspace.shape), torch.uint8, dev), workspace.numel(),
+        _current_stream(dev)), "moe_expert_swiglu_fp8")
     return expert_out
 
 
@@ -811,15 +820,15 @@ def layer(logits: torch.Tensor, x: torch.Tensor, k: int, w_gate_up: torch.Tensor
     if workspace is None:
         workspace = _workspace(None, int(lib().moe_layer_workspace_bytes(sh, I)), dev)
     _check(lib().moe_layer(
-        sh, I, MOE_F8E4M3 if fp8 else MOE_BF16, _checked("logits", logits, (T, E), f32),
-        _checked("x", x, (T, H), bf16), _checked("w_gate_up", w_gate_up, (E, 2 * I, H), wtype),
-        _checked("s_gate_up", s_gate_up, (E, _blocks(2 * I), _blocks(H)), f32) if fp8 else None,
-        _checked("w_down", w_down, (E, H, I), wtype),
-        _checked("s_down", s_down, (E, _blocks(H), _blocks(I)), f32) if fp8 else None,
-        _checked("topk_idx", topk_idx, (T, k), torch.int32), _checked("topk_w", topk_w, (T, k), f32),
-        _checked("y", y, (T, H), bf16),
-        _checked("workspace", workspace, tuple(workspace.shape), torch.uint8), workspace.numel(),
-        _current_stream()), "moe_layer")
+        sh, I, MOE_F8E4M3 if fp8 else MOE_BF16, _checked("logits", logits, (T, E), f32, dev),
+        _checked("x", x, (T, H), bf16, dev), _checked("w_gate_up", w_gate_up, (E, 2 * I, H), wtype, dev),
+        _checked("s_gate_up", s_gate_up, (E, _blocks(2 * I), _blocks(H)), f32, dev) if fp8 else None,
+        _checked("w_down", w_down, (E, H, I), wtype, dev),
+        _checked("s_down", s_down, (E, _blocks(H), _blocks(I)), f32, dev) if fp8 else None,
+        _checked("topk_idx", topk_idx, (T, k), torch.int32, dev), _checked("topk_w", topk_w, (T, k), f32, dev),
+        _checked("y", y, (T, H), bf16, dev),
+        _checked("workspace", workspace, tuple(workspace.shape), torch.uint8, dev), workspace.numel(),
+        _current_stream(dev)), "moe_layer")
     return y, topk_idx, topk_w
 
 
