@@ -27,6 +27,8 @@
 namespace moe {
 namespace {
 
+constexpr int kMaxExperts = 1024;
+constexpr int kUnitsPerXcd = 32;  // compute units
 constexpr int kBK = 128;    // K step: one scale block, one 128-byte tile row
 
 // LDS tile: rows of 128 bytes = eight 16-byte chunks; chunk c of row r sits at
@@ -47,10 +49,69 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* lds
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)lds, 4, voff, soff, 0, 0);
 }
 
-// BM x BN block tile of WM x WN waves, each (BM/WM) x (BN/WN) as MI x NI
-// fragments of 16 x 16. N: rows of one expert's B (2 I for gate/up).
-template <bool kGateUp, int BM, int BN, int OCC, int WM, int WN>
-__global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
+// m-tile prefix sums of the experts in LDS: pre[e] m-tiles before expert e, pre[E] in
+// all. Counts outside [0, rows_total] give no tile. Called by the whole block.
+template <int BM>
+__device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ cnts, int E,
+                                            int64_t rows_total, int* pre) {
+  if (threadIdx.x < kWave) {
+    const int lane = threadIdx.x;
+    const int c = (E + kWave - 1) / kWave;  // lane l scans experts [l*c, l*c + c)
+    const int e0 = lane * c, e1 = (e0 + c < E) ? e0 + c : E;
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) {
+      const int n = cnts[e];
+      mine += n > 0 && n <= rows_total ? (n + BM - 1) / BM : 0;
+      pre[e + 1] = mine;
+    }
+    int incl = mine;
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int y = __shfl_up(incl, o);
+      if (lane >= o) incl += y;
+    }
+    for (int e = e0; e < e1; ++e) pre[e + 1] += incl - mine;
+    if (lane == 0) pre[0] = 0;
+  }
+  __syncthreads();
+}
+
+// Tile number lin of the list (patches of kGroupM m-tiles by all n-tiles); e < 0
+// where the expert's rows do not lie in [0, rows_total). Uniform, no barrier.
+template <int BM>
+__device__ __forceinline__ Tile tile_at_place(const int* pre, const int32_t* __restrict__ offs,
+                                              const int32_t* __restrict__ cnts, int E,
+                                              int64_t rows_total, int ntiles, int lin) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int MT = __builtin_amdgcn_readfirstlane(pre[E]);
+  const int grp = lin / (kGroupM * ntiles), r = lin - grp * kGroupM * ntiles;
+  const int gh = MT - grp * kGroupM < kGroupM ? MT - grp * kGroupM : kGroupM;
+  const int ntile = r / gh, mt = grp * kGroupM + (r - ntile * gh);
+  // the expert with pre[e] <= mt < pre[e + 1]: the 64th of the experts, then in it
+  const int c = (E + kWave - 1) / kWave;
+  const int hi = (lane + 1) * c < E ? (lane + 1) * c : E;
+  const int part = __popcll(__ballot(pre[hi] <= mt));
+  const int at = part * c + 1 + lane;
+  const int e = part * c + __popcll(__ballot(lane < c && at <= E && pre[at < E ? at : E] <= mt));
+  const int m0 = (mt - __builtin_amdgcn_readfirstlane(pre[e])) * BM;
+  const int left = cnts[e] - m0, rows = left < BM ? left : BM;
+  const int64_t first = (int64_t)offs[e] + m0;
+  const bool ok = first >= 0 && first + rows <= rows_total;
+  return {ok ? e : -1, ok ? (int)first : 0, ok ? rows : 0, ntile};
+}
+
+// A block barrier behind this wave's LDS operations, not its loads.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Block tiles of BM x BN by WM x WN waves, each wave (BM/WM) x (BN/WN) as MI x NI
+// fragments of 16 x 16. N: rows of one expert's B (2 I for gate/up). One block a
+// compute unit; it takes every gridDim.x / 8-th tile of its XCD's share of the
+// list (contiguous, so the XCD's L2 serves its rows and weights), and the K steps of its
+// tiles are one stream: the loads run two steps ahead, into the next tile's first
+// steps while this one's last run and its results are stored.
+template <bool kGateUp, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ Asc,
     const int32_t* __restrict__ offs, const int32_t* __restrict__ cnts, int E,
     int64_t rows_total, const uint8_t* __restrict__ B, const float* __restrict__ Bsc, int N, int K,
@@ -65,7 +126,8 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
   // separate arrays: the loads into one stage and the reads of the other do not alias
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[kStage];
-  __shared__ int info[4];
+  __shared__ uint32_t ex[kGateUp ? WN * BM : 1];  // row maxima of h, a wave column each
+  __shared__ int pre[kMaxExperts + 1];
   const auto stage = [&](auto S) -> uint8_t* {
     if constexpr (decltype(S)::value % 2 == 0) return lds0;
     else return lds1;
@@ -73,20 +135,43 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wid / WN, wn = wid % WN;
-  const Tile tile = find_tile<BM>(offs, cnts, E, rows_total, ntiles, info);
-  if (tile.e < 0) return;  // uniform over the block
-  const int e = tile.e, row0 = tile.row0, rows = tile.rows, ntile = tile.ntile;
-  // waves whose rows all lie past the tile's last one only load and meet the barriers
-  const bool live = wm * (BM / WM) < rows;
   const int KB = K / kBK, I = N / 2, NB = (N + kQuantBlock - 1) / kQuantBlock;
 
+  // ---- the block's tiles: places place, place + hop, ... below limit
+  tile_prefix<BM>(cnts, E, rows_total, pre);
+  const int total = __builtin_amdgcn_readfirstlane(pre[E]) * ntiles;
+  const int per = (total + kXCD - 1) / kXCD;
+  const int hop = gridDim.x / kXCD;
+  const int xcd = blockIdx.x % kXCD;
+  const int limit = (xcd + 1) * per < total ? (xcd + 1) * per : total;
+  int place = xcd * per + blockIdx.x / kXCD;
+  if (place >= limit) return;  // uniform over the block
+  const auto tile_of = [&](int p) {
+    if (p >= limit) return Tile{-1, 0, 0, 0};
+    return tile_at_place<BM>(pre, offs, cnts, E, rows_total, ntiles, p);
+  };
+
   // ---- loads: one wave instruction fills eight 128-byte tile rows, lane l the
-  // slot l % 8 of row l / 8; rows past the last one are out of the descriptor's
-  // range and read as zeros.
-  const __amdgpu_buffer_rsrc_t arsrc = make_rsrc(A + (int64_t)row0 * K, (int64_t)rows * K);
-  const __amdgpu_buffer_rsrc_t brsrc = make_rsrc(B + (int64_t)e * N * K, (int64_t)N * K);
-  const __amdgpu_buffer_rsrc_t srsrc =
-      make_rsrc(Asc + (int64_t)row0 * KB, (int64_t)rows * KB * 4);
+  // slot l % 8 of row l / 8. The descriptors begin at the tile (of B: at its
+  // first weight row), so the lanes' offsets are the same for every tile; rows past the last
+  // one are out of range and read as zeros.
+  struct Source {
+    const uint8_t *a, *b;
+    const float* sc;
+    uint32_t abytes, bbytes, sbytes;
+  };
+  // (No tile: the first rows and weights, which nothing uses. A descriptor is never
+  // shorter than the K step's offset that is added to it.)
+  const auto source_of = [&](const Tile& t) -> Source {
+    const int n0 = t.e < 0 ? 0 : t.ntile * NO;
+    const int rows = t.e < 0 ? (rows_total < BM ? (int)rows_total : BM) : t.rows;
+    return {A + (int64_t)t.row0 * K,
+            B + ((int64_t)(t.e < 0 ? 0 : t.e) * N + n0) * K,
+            Asc + (int64_t)t.row0 * KB,
+            (uint32_t)rows * (uint32_t)K,
+            (uint32_t)(N - n0) * (uint32_t)K,
+            (uint32_t)rows * (uint32_t)KB * 4};
+  };
   uint32_t aoff[AI], boff[BI];
 #pragma unroll
   for (int i = 0; i < AI; ++i) {
@@ -96,22 +181,35 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
 #pragma unroll
   for (int i = 0; i < BI; ++i) {
     const int r = wid * (BN / NW) + 8 * i + (lane >> 3);
-    int n;
-    if constexpr (kGateUp) n = r < NO ? ntile * NO + r : I + ntile * NO + (r - NO);
-    else n = ntile * BN + r;
+    const int n = kGateUp && r >= NO ? I + r - NO : r;
     boff[i] = (uint32_t)n * (uint32_t)K + (((lane & 7) ^ b_key(r)) << 4);
   }
   const int srow = wid % (BM / 64) * 64;  // the 64 row scales this wave loads
   const uint32_t soff = (uint32_t)(srow + lane) * (uint32_t)KB * 4;
   constexpr int kLoads = AI + BI + 1;
-  // load number q of a step's kLoads
-  auto issue = [&](uint8_t* st, int kt, int q) __attribute__((always_inline)) {
+  Source src, after;  // of what is loaded now, and of the tile after the one computed
+  int lk = 0;         // K step that is loaded
+  // load number q of the step's kLoads
+  auto issue = [&](uint8_t* st, int q) __attribute__((always_inline)) {
     if (q < BI)
-      load_lds(brsrc, st + (BM + wid * (BN / NW) + 8 * q) * kBK, boff[q % BI], kt * kBK);
+      load_lds(make_rsrc(src.b, src.bbytes), st + (BM + wid * (BN / NW) + 8 * q) * kBK,
+               boff[q % BI], lk * kBK);
     else if (q < BI + AI)
-      load_lds(arsrc, st + (wid * (BM / NW) + 8 * (q - BI)) * kBK, aoff[(q - BI) % AI], kt * kBK);
+      load_lds(make_rsrc(src.a, src.abytes), st + (wid * (BM / NW) + 8 * (q - BI)) * kBK,
+               aoff[(q - BI) % AI], lk * kBK);
     else
-      load_lds4(srsrc, st + (BM + BN) * kBK + srow * 4, soff, kt * 4);
+      load_lds4(make_rsrc(src.sc, src.sbytes), st + (BM + BN) * kBK + srow * 4, soff, lk * 4);
+  };
+  // K >= 2 steps, so the loads enter the next tile once while a tile is computed
+  auto next_load = [&]() __attribute__((always_inline)) {
+    const bool wrap = ++lk == KB;
+    lk = wrap ? 0 : lk;
+    src.a = wrap ? after.a : src.a;
+    src.b = wrap ? after.b : src.b;
+    src.sc = wrap ? after.sc : src.sc;
+    src.abytes = wrap ? after.abytes : src.abytes;
+    src.bbytes = wrap ? after.bbytes : src.bbytes;
+    src.sbytes = wrap ? after.sbytes : src.sbytes;
   };
 
   // ---- fragments: lane l holds row (l % 16), chunks l / 16 and l / 16 + 4 of its
@@ -143,69 +241,65 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
     return *reinterpret_cast<const float*>(st + (BM + BN) * kBK + (arow + mi * 16) * 4);
   };
 
-  // Weight scales of this wave's column block(s): lane l holds K block kt0 + l,
-  // read out by lane index, reloaded every 64 steps.
-  const int ncol = ntile * NO + wn * (NO / WN);  // first output column of the wave
-  int nb0 = ncol / kQuantBlock;
-  if (nb0 > NB - 1) nb0 = NB - 1;
-  const float* bs0 = Bsc + ((int64_t)e * NB + nb0) * KB;
-  const float* bs1 = kGateUp ? bs0 + (int64_t)(I / kQuantBlock) * KB : bs0;
-  float sv0 = 0.f, sv1 = 0.f;
-  auto load_bs = [&](int kt0) __attribute__((always_inline)) {
-    const int i = kt0 + lane < KB ? kt0 + lane : KB - 1;
-    sv0 = bs0[i];
-    if constexpr (kGateUp) sv1 = bs1[i];
-    // landed here and now: a use in the step loop would otherwise wait for the
-    // step's own loads too (the counter is in order)
-    asm volatile("" : "+v"(sv0), "+v"(sv1));
+  // ---- the tile being computed
+  Tile tile = tile_of(place);
+  bool live;            // this wave has rows in it: the others only load and meet the barriers
+  int ncol;             // first output column of the wave
+  const float *bs0, *bs1;  // weight scales of its column block(s), one a K step
+  auto enter = [&](const Tile& t) __attribute__((always_inline)) {
+    tile = t;
+    live = wm * (BM / WM) < t.rows;
+    ncol = t.ntile * NO + wn * (NO / WN);
+    const int nb = ncol / kQuantBlock < NB ? ncol / kQuantBlock : NB - 1;
+    bs0 = Bsc + ((int64_t)(t.e < 0 ? 0 : t.e) * NB + nb) * KB;
+    bs1 = kGateUp ? bs0 + (int64_t)(I / kQuantBlock) * KB : bs0;
   };
-  auto lane_f = [&](float v, int l) {
-    return __uint_as_float(lane_value(__float_as_uint(v), l));
-  };
+  enter(tile);
 
   f32x4 acc[NI][MI];
-#pragma unroll
-  for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) acc[ni][mi] = f32x4{0, 0, 0, 0};
-
   i32x8 fa[MI], fb[4];
   float sa[MI];
-  load_bs(0);
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int q = 0; q < kLoads; ++q) issue(lds0, 0, q);
+    for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-  for (int q = 0; q < kLoads; ++q) issue(lds1, KB > 1 ? 1 : 0, q);
-  __builtin_amdgcn_s_waitcnt(wait_vmcnt(kLoads));
-  __syncthreads();
+      for (int mi = 0; mi < MI; ++mi) acc[ni][mi] = f32x4{0, 0, 0, 0};
+  };
+  auto first_frags = [&](const uint8_t* st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      fa[mi] = read_a(st, mi);
+      sa[mi] = read_s(st, mi);
+    }
+    fb[0] = read_b(st, 0);
+    fb[1] = read_b(st, 1);
+  };
 
-  // Step kt reads stage kt % 2. Its fragments of A, the row scales and the first
-  // two fragments of B are in registers already. Once a wave has read the last
-  // fragments of the stage and its loads of step kt+1 have landed, there is one
-  // barrier; the MFMAs of the last two columns run behind it, so that the first
-  // fragments of step kt+1 are read while they do. The loads of step kt+2 into the
-  // stage are spread: kAfter of them among those MFMAs, the rest one every second
-  // MFMA of the next step. All at once after the barrier, the eight waves' 72 loads
-  // (16 cycles each in the address unit) held up the MFMAs behind them (8192 x 4096
-  // x 7168: 221 against 213 us; spread over the next step alone 245, too late).
-  // Past the last step the loads repeat it into a stage nobody reads again.
-  // Each MFMA's result is folded two MFMAs later; the issue priority is raised
-  // for the columns before the barrier (gate/up 455 against 415 us, also because the
+  // A step reads stage S. Its fragments of A, the row scales and the first two
+  // fragments of B are in registers already. Once a wave has read the last
+  // fragments of the stage and its loads of the next step have landed, there is
+  // one barrier; the MFMAs of the last two columns run behind it, so that the first
+  // fragments of the next step are read while they do. The loads of the step after
+  // next into this stage are spread: kAfter of them among those MFMAs, the rest one every
+  // second MFMA of the next step. All at once after the barrier, the eight waves'
+  // 72 loads (16 cycles each in the address unit) held up the MFMAs behind them
+  // (8192 x 4096 x 7168: 221 against 213 us; spread over the next step alone 245,
+  // too late). Each MFMA's result is folded two MFMAs later; the issue priority is
+  // raised for the columns before the barrier (gate/up 455 against 415 us, also because the
   // scheduling fence keeps the registers from spilling).
+  constexpr int kAfter = 5;
   auto step = [&](auto S, int kt) __attribute__((always_inline)) {
     uint8_t* cur = stage(S);
     uint8_t* nxt = stage(std::integral_constant<int, decltype(S)::value + 1>{});
-    if ((kt & 63) == 0 && kt > 0) load_bs(kt);
-    const float w0 = lane_f(sv0, kt & 63), w1 = kGateUp ? lane_f(sv1, kt & 63) : 0.f;
+    const float w0 = bs0[kt], w1 = bs1[kt];
     float s0[MI], s1[MI];
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       s0[mi] = sa[mi] * w0;
       s1[mi] = kGateUp ? sa[mi] * w1 : s0[mi];
     }
-    constexpr int kRing = 4, kLag = 2;                     // results in flight
+    constexpr int kRing = 4, kLag = 2;                      // results in flight
     constexpr int kBefore = (NI - 2) * MI, kAll = NI * MI;  // MFMAs before the barrier, in all
-    constexpr int kAfter = 5;                              // loads among those after it
     auto ni_of = [](int j) { return j < kBefore ? j / MI : NI - 2 + (j - kBefore) % 2; };
     auto mi_of = [](int j) { return j < kBefore ? j % MI : (j - kBefore) / 2; };
     f32x4 t[kRing];
@@ -213,8 +307,8 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
       const int ni = ni_of(j), mi = mi_of(j);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        acc[ni][mi][r] = __builtin_fmaf(t[j % kRing][r], kGateUp && ni >= NI / 2 ? s1[mi] : s0[mi],
-                                        acc[ni][mi][r]);
+        acc[ni][mi][r] = __builtin_fmaf(
+            t[j % kRing][r], kGateUp && ni >= NI / 2 ? s1[mi] : s0[mi], acc[ni][mi][r]);
     };
     auto mma = [&](int j) __attribute__((always_inline)) {
       t[j % kRing] = mfma_fp8(fb[ni_of(j) % 4], fa[mi_of(j)]);
@@ -228,11 +322,11 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
       for (int mi = 0; mi < MI; ++mi) {
         const int j = ni * MI + mi, q = kAfter + j / 2;
         mma(j);
-        // (step 1 is loaded whole before the first one)
-        if (j % 2 == 0 && q < kLoads && kt > 0) issue(nxt, kt + 1 < KB ? kt + 1 : KB - 1, q);
+        if (j % 2 == 0 && q < kLoads) issue(nxt, q);
       }
     }
     __builtin_amdgcn_s_setprio(0);
+    next_load();
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
     __syncthreads();
 #pragma unroll
@@ -241,7 +335,7 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
       mma(kBefore + 2 * mi + 1);
 #pragma unroll
       for (int q = 0; q < kAfter; ++q)
-        if (q * MI / kAfter == mi) issue(cur, kt + 2 < KB ? kt + 2 : KB - 1, q);
+        if (q * MI / kAfter == mi) issue(cur, q);
       fa[mi] = read_a(nxt, mi);
       sa[mi] = read_s(nxt, mi);
       if (mi < 2) fb[mi] = read_b(nxt, mi);
@@ -249,112 +343,135 @@ __global__ __launch_bounds__(kWave * WM * WN, OCC) void gemm_fp8_kernel(
 #pragma unroll
     for (int j = kAll - kLag; j < kAll; ++j) fold(j);
   };
+  // The same loads and barrier of a wave without rows in the tile.
+  auto dead_step = [&](uint8_t* cur, uint8_t* nxt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = kAfter; q < kLoads; ++q) issue(nxt, q);
+    next_load();
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kAfter; ++q) issue(cur, q);
+  };
+
+  // ---- results: the stores go through descriptors over the tile's rows, whose
+  // range check drops the rows past the last one.
+  auto finish = [&]() __attribute__((always_inline)) {
+    const int g = lane >> 4;
+    if constexpr (!kGateUp) {
+      const __amdgpu_buffer_rsrc_t crsrc = make_rsrc(
+          static_cast<uint16_t*>(C) + (int64_t)tile.row0 * N, (int64_t)tile.rows * N * 2);
+#pragma unroll
+      for (int p = 0; p < NI / 2; ++p) {
+        const int n = ncol + 32 * p + 8 * g;
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+          const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
+          const v4u v = {bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]),
+                         bf16x2_rne(hi[0], hi[1]), bf16x2_rne(hi[2], hi[3])};
+          // columns past N would wrap into the next row: offset out of range instead
+          const uint32_t off = n < N ? ((uint32_t)(arow + mi * 16) * (uint32_t)N + n) * 2 : kOutside;
+          __builtin_amdgcn_raw_buffer_store_b128(v, crsrc, off, 0, 0);
+        }
+      }
+    } else {
+      // h = SiLU(g) u in place of g; the row maximum over the tile's 128 columns:
+      // this lane's, the other lanes' of the row (16 and 32 apart), the other
+      // waves' through LDS. Rows are whole scale blocks of h.
+      {
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int ni = 0; ni < NI / 2; ++ni)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float h = silu(acc[ni][mi][r]) * acc[ni + NI / 2][mi][r];
+              acc[ni][mi][r] = h;
+              const uint32_t u = finite_bits(h);
+              m = u > m ? u : m;
+            }
+          uint32_t o = (uint32_t)__shfl_xor((int)m, 16);
+          m = o > m ? o : m;
+          o = (uint32_t)__shfl_xor((int)m, 32);
+          m = o > m ? o : m;
+          if (g == 0) ex[wn * BM + arow + mi * 16] = m;
+        }
+      }
+      lds_barrier();  // the maxima are read before the next step's barrier, so before they change
+      const __amdgpu_buffer_rsrc_t crsrc =
+          make_rsrc(static_cast<uint8_t*>(C) + (int64_t)tile.row0 * I, (int64_t)tile.rows * I);
+      const int IB = I / kQuantBlock;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const int m = arow + mi * 16;
+        uint32_t a = 0;
+#pragma unroll
+        for (int w = 0; w < WN; ++w) a = ex[w * BM + m] > a ? ex[w * BM + m] : a;
+        const int p2 = scale_exponent(a);
+        const float inv = power_of_two(-p2);
+        if (g == 0 && wn == 0 && m < tile.rows)
+          Csc[(int64_t)(tile.row0 + m) * IB + tile.ntile] = power_of_two(p2);
+#pragma unroll
+        for (int p = 0; p < NI / 4; ++p) {
+          const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
+          const uint32_t q0 = e4m3x4(e4m3_clamp(lo[0] * inv), e4m3_clamp(lo[1] * inv),
+                                     e4m3_clamp(lo[2] * inv), e4m3_clamp(lo[3] * inv));
+          const uint32_t q1 = e4m3x4(e4m3_clamp(hi[0] * inv), e4m3_clamp(hi[1] * inv),
+                                     e4m3_clamp(hi[2] * inv), e4m3_clamp(hi[3] * inv));
+          typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+          __builtin_amdgcn_raw_buffer_store_b64(v2u{q0, q1}, crsrc,
+                                                (uint32_t)m * (uint32_t)I + ncol + 32 * p + 8 * g, 0, 0);
+        }
+      }
+    }
+  };
+  // Steps 0 and (the first kAfter loads) 1 of the stream, then tile by tile; par: the
+  // stage of the tile's first step.
+  src = after = source_of(tile);
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) issue(lds0, q);
+  next_load();
+#pragma unroll
+  for (int q = 0; q < kAfter; ++q) issue(lds1, q);
+  __builtin_amdgcn_s_waitcnt(wait_vmcnt(kAfter));
+  __syncthreads();
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  if (live) {
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      fa[mi] = read_a(lds0, mi);
-      sa[mi] = read_s(lds0, mi);
-    }
-    fb[0] = read_b(lds0, 0);
-    fb[1] = read_b(lds0, 1);
-    int kt = 0;
-    for (; kt + 2 <= KB; kt += 2) {
-      step(I0{}, kt);
-      step(I1{}, kt + 1);
-    }
-    if (kt < KB) step(I0{}, kt);
-  } else {
-    // the same barriers and loads
-    for (int kt = 0; kt < KB; ++kt) {
-      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kLoads; ++q) issue(kt & 1 ? lds1 : lds0, kt + 2 < KB ? kt + 2 : KB - 1, q);
-    }
-  }
-  // the trailing loads must land before the block's LDS is reused or released
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-
-  // ---- epilogue: the stores go through descriptors over the tile's rows, whose
-  // range check drops the rows past the last one.
-  const int g = lane >> 4;
-  if constexpr (!kGateUp) {
-    if (!live) return;
-    const __amdgpu_buffer_rsrc_t crsrc =
-        make_rsrc(static_cast<uint16_t*>(C) + (int64_t)row0 * N, (int64_t)rows * N * 2);
-#pragma unroll
-    for (int p = 0; p < NI / 2; ++p) {
-      const int n = ncol + 32 * p + 8 * g;
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
-        const v4u v = {bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]),
-                       bf16x2_rne(hi[0], hi[1]), bf16x2_rne(hi[2], hi[3])};
-        // columns past N would wrap into the next row: offset out of range instead
-        const uint32_t off = n < N ? ((uint32_t)(arow + mi * 16) * (uint32_t)N + n) * 2 : 0xFFFFFFF0u;
-        __builtin_amdgcn_raw_buffer_store_b128(v, crsrc, off, 0, 0);
-      }
-    }
-  } else {
-    // h = SiLU(g) u in place of g; the row maximum over the tile's 128 columns:
-    // this lane's, the other lanes' of the row (16 and 32 apart), the other
-    // waves' through LDS. Rows are whole scale blocks of h.
-    uint32_t* ex = reinterpret_cast<uint32_t*>(lds0);  // [WN][BM]
-    uint32_t am[MI];
-    __syncthreads();  // every wave is done with the stages
+  for (int par = 0;;) {
+    const Tile ahead = tile_of(place + hop);
+    after = source_of(ahead);
     if (live) {
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int ni = 0; ni < NI / 2; ++ni)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float h = silu(acc[ni][mi][r]) * acc[ni + NI / 2][mi][r];
-            acc[ni][mi][r] = h;
-            const uint32_t u = finite_bits(h);
-            m = u > m ? u : m;
-          }
-        uint32_t o = (uint32_t)__shfl_xor((int)m, 16);
-        m = o > m ? o : m;
-        o = (uint32_t)__shfl_xor((int)m, 32);
-        m = o > m ? o : m;
-        if (g == 0) ex[wn * BM + arow + mi * 16] = m;
+      clear();
+      first_frags(par ? lds1 : lds0);
+      int kt = 0;
+      if (par) step(I1{}, kt++);
+      for (; kt + 2 <= KB; kt += 2) {
+        step(I0{}, kt);
+        step(I1{}, kt + 1);
       }
-    }
-    __syncthreads();
-    if (!live) return;
-    const __amdgpu_buffer_rsrc_t crsrc =
-        make_rsrc(static_cast<uint8_t*>(C) + (int64_t)row0 * I, (int64_t)rows * I);
-    const int IB = I / kQuantBlock;
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      const int m = arow + mi * 16;
-      uint32_t a = 0;
-#pragma unroll
-      for (int w = 0; w < WN; ++w) a = ex[w * BM + m] > a ? ex[w * BM + m] : a;
-      am[mi] = a;
-      const int p2 = scale_exponent(am[mi]);
-      const float inv = power_of_two(-p2);
-      if (g == 0 && wn == 0 && m < rows) Csc[(int64_t)(row0 + m) * IB + ntile] = power_of_two(p2);
-#pragma unroll
-      for (int p = 0; p < NI / 4; ++p) {
-        const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
-        const uint32_t q0 = e4m3x4(e4m3_clamp(lo[0] * inv), e4m3_clamp(lo[1] * inv),
-                                   e4m3_clamp(lo[2] * inv), e4m3_clamp(lo[3] * inv));
-        const uint32_t q1 = e4m3x4(e4m3_clamp(hi[0] * inv), e4m3_clamp(hi[1] * inv),
-                                   e4m3_clamp(hi[2] * inv), e4m3_clamp(hi[3] * inv));
-        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-        __builtin_amdgcn_raw_buffer_store_b64(v2u{q0, q1}, crsrc,
-                                              (uint32_t)m * (uint32_t)I + ncol + 32 * p + 8 * g, 0, 0);
+      if (kt < KB) step(I0{}, kt);
+      // The loads that run ahead land here, where it costs the least: past this point
+      // nothing is pending in either stage, whichever the next tile begins with.
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+      finish();
+    } else {
+      for (int kt = 0; kt < KB; ++kt) {
+        if ((kt + par) & 1) dead_step(lds1, lds0);
+        else dead_step(lds0, lds1);
       }
+      if constexpr (kGateUp) lds_barrier();  // the one in finish()
     }
+    par = (par + KB) & 1;
+    place += hop;
+    if (place >= limit) break;
+    enter(ahead);
   }
+  // the trailing loads must land before the block's LDS is released
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
 }
 
-template <bool kGateUp, int BM, int BN, int OCC, int WM, int WN>
+template <bool kGateUp, int BM, int BN, int WM, int WN>
 hipError_t run_gemm(const void* a, const float* asc, int64_t rows, int E, const int32_t* offs,
                     const int32_t* cnts, const void* w, const float* wsc, int N, int K, void* c,
                     float* csc, hipStream_t s) {
@@ -363,8 +480,9 @@ hipError_t run_gemm(const void* a, const float* asc, int64_t rows, int E, const 
   const int ntiles = (cols + NO - 1) / NO;
   // every expert with rows adds at most one partial m-tile
   const int64_t mt = rows / BM + (rows < E ? rows : E);
-  const int64_t per = (mt * ntiles + kXCD - 1) / kXCD;
-  return launch(gemm_fp8_kernel<kGateUp, BM, BN, OCC, WM, WN>, dim3((unsigned)(per * kXCD)),
+  int64_t per = (mt * ntiles + kXCD - 1) / kXCD;
+  if (per > kUnitsPerXcd) per = kUnitsPerXcd;  // one block a compute unit
+  return launch(gemm_fp8_kernel<kGateUp, BM, BN, WM, WN>, dim3((unsigned)(per * kXCD)),
                 dim3(kWave * WM * WN), 0, s, static_cast<const uint8_t*>(a), asc, offs, cnts, E,
                 rows, static_cast<const uint8_t*>(w), wsc, N, K, c, csc, ntiles);
 }
@@ -373,8 +491,9 @@ hipError_t run_gemm(const void* a, const float* asc, int64_t rows, int E, const 
 // are the faster. 128 experts, N 2816, K 4096, even routing: 16 rows 258 against
 // 323 us, 24 rows 291 against 327, 32 rows (half the experts take two tiles) 416
 // against 332; K 1408, N 4096: 16 rows 140 against 171, 32 rows 228 against 182.
+// One K step is too short for the tiled kernel's stream of loads.
 constexpr int kFewRows = 24;
-bool few_rows(int64_t rows, int E) { return rows <= (int64_t)kFewRows * E; }
+bool few_rows(int64_t rows, int E, int K) { return K == kBK || rows <= (int64_t)kFewRows * E; }
 
 }  // namespace
 
@@ -382,9 +501,9 @@ hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
                            const int32_t* offs, const int32_t* cnts, const void* w,
                            const float* wsc, int N, int K, void* out, hipStream_t s) {
   if (rows == 0) return hipSuccess;
-  if (few_rows(rows, E))
+  if (few_rows(rows, E, K))
     return launch_gemm_fp8_stream(false, a, asc, rows, E, offs, cnts, w, wsc, N, K, out, nullptr, s);
-  return run_gemm<false, 256, 256, 1, 4, 2>(a, asc, rows, E, offs, cnts, w, wsc, N, K, out, nullptr,
+  return run_gemm<false, 256, 256, 4, 2>(a, asc, rows, E, offs, cnts, w, wsc, N, K, out, nullptr,
                                             s);
 }
 
@@ -395,10 +514,10 @@ hipError_t launch_expert_swiglu_fp8(const void* send, const float* ssc, int64_t 
                                     hipStream_t s) {
   if (rows == 0) return hipSuccess;
   const hipError_t err =
-      few_rows(rows, E)
+      few_rows(rows, E, H)
           ? launch_gemm_fp8_stream(true, send, ssc, rows, E, offs, cnts, w_gate_up, gsc, 2 * I, H, hq,
                                    hs, s)
-          : run_gemm<true, 256, 256, 1, 4, 2>(send, ssc, rows, E, offs, cnts, w_gate_up, gsc, 2 * I,
+          : run_gemm<true, 256, 256, 4, 2>(send, ssc, rows, E, offs, cnts, w_gate_up, gsc, 2 * I,
                                               H, hq, hs, s);
   if (err != hipSuccess) return err;
   return launch_gemm_fp8(hq, hs, rows, E, offs, cnts, w_down, dsc, H, I, out, s);

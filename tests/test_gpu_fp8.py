@@ -141,6 +141,10 @@ GEMM = [
     ([1], 0, 16, 128), ([1], 0, 256, 256), ([300], 0, 272, 384), ([0, 1, 0, 2, 255, 256, 257], 0, 128, 128),
     ([3, 0, 17, 64, 65], 5, 144, 640), ([16] * 9, 0, 2816, 1408), ([513, 1], 3, 1024, 512),
     ([5] * 70, 0, 48, 256), ([40, 33, 0, 12], 0, 512, 8448), ([700], 0, 640, 128),
+    # several tiles a compute unit: two, three and five K steps, row tiles of few
+    # rows between full ones, columns past the last tile, K steps beyond 64
+    ([3000], 0, 8192, 256), ([2900], 0, 7952, 384), ([700, 0, 513, 1, 1, 600], 2, 4112, 640),
+    ([30, 0, 29, 257, 1] * 9, 0, 2064, 384), ([90, 40], 0, 272, 8576), ([33] * 300, 1, 256, 256),
 ]
 
 
@@ -193,7 +197,8 @@ def test_expert_gemm_fp8_nan_stays_in_its_row():
 
 @pytest.mark.parametrize("counts,H,I", [
     ([1], 128, 128), ([0, 3, 260, 0, 1], 256, 384), ([17, 64, 1], 1024, 128),
-    ([6] * 20, 384, 1408), ([300, 280], 512, 256)])
+    ([6] * 20, 384, 1408), ([300, 280], 512, 256), ([60, 0, 300, 1, 20] * 5, 256, 1408),
+    ([2100], 384, 2176), ([30, 270] * 3, 128, 640)])
 def test_expert_swiglu_fp8(counts, H, I):
     print(f"[swiglu fp8] counts={counts[:6]} H={H} I={I}", flush=True)
     E, rows = len(counts), sum(counts)
