@@ -783,8 +783,8 @@ int moe_quantize(const void* x, int32_t dtype, int32_t batch, int32_t rows, int3
   if (batch < 0 || rows < 0 || cols < 1 || (block_rows != 1 && block_rows != 128))
     return MOE_ERR_ARG;
   if (cols % 16 != 0) return MOE_ERR_ALIGN;
-  // 16-element vectors are counted in 32 bits
-  const int64_t vecs = 8 * ceil_div(cols, 128);
+  // 16-byte vectors are counted in 32 bits
+  const int64_t vecs = (dtype == MOE_BF16 ? 16 : 32) * ceil_div(cols, 128);
   if (int64_t(batch) * rows >= kIndexLimit || int64_t(batch) * rows * vecs >= kIndexLimit)
     return MOE_ERR_ARG;
   if (batch > 0 && rows > 0 && (!x || !q || !scale)) return MOE_ERR_ARG;
@@ -798,7 +798,8 @@ int moe_dispatch_copy_fp8(const moe_shape* shape, const void* x, const int32_t* 
   const int st = check_shape(shape);
   if (st != MOE_OK) return st;
   if (shape->H % 16 != 0) return MOE_ERR_ALIGN;
-  if (int64_t(shape->T) * 8 * ceil_div(shape->H, 128) >= kIndexLimit) return MOE_ERR_ARG;
+  if (int64_t(shape->T) * (shape->dtype == MOE_BF16 ? 16 : 32) * ceil_div(shape->H, 128) >= kIndexLimit)
+    return MOE_ERR_ARG;
   if (shape->T > 0 && (!x || !pos || !send_q || !send_scale)) return MOE_ERR_ARG;
   if (!aligned(x, 16) || !aligned(send_q, 16) || !aligned(pos, 4) || !aligned(send_scale, 4))
     return MOE_ERR_ALIGN;

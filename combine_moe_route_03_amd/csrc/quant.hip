@@ -17,57 +17,66 @@ namespace {
 
 constexpr int kBlock = 256;
 
-// Rows: eight consecutive lanes hold one group of 128 columns, 16 elements a
-// lane (one 16-byte store of e4m3 each). Flat over (row, group, lane of the
-// group); the last group of a row may be short (cols % 128, a multiple of 16).
+// Streaming store of a lane's e4m3 bytes.
+__device__ __forceinline__ void store_q(void* p, uint2 v) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(v2u{v.x, v.y}, static_cast<v2u*>(p));
+}
+__device__ __forceinline__ void store_q(void* p, uint32_t v) {
+  __builtin_nontemporal_store(v, static_cast<uint32_t*>(p));
+}
+
+// Rows: QuantVec::kLanes consecutive lanes hold one group of 128 columns. Flat over
+// (row, group, lane of the group); the last group of a row may be short (cols %
+// 128, a multiple of 16). nvec: 16-byte vectors of a row.
 template <bool kBF16>
 __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const v4u* __restrict__ x,
                                                                uint32_t total, uint32_t groups,
-                                                               uint32_t nvec, v4u* __restrict__ q,
+                                                               uint32_t nvec, uint8_t* __restrict__ q,
                                                                float* __restrict__ scale) {
+  typedef QuantVec<kBF16> Vec;
   const uint32_t i = blockIdx.x * (uint32_t)kBlock + threadIdx.x;
-  const uint32_t grp = i >> 3;  // group of the whole array: row * groups + group
+  const uint32_t grp = i / Vec::kLanes;  // group of the whole array: row * groups + group
   const uint32_t row = grp / groups;
-  const uint32_t col = (grp - row * groups) * 8 + (i & 7);
+  const uint32_t col = (grp - row * groups) * Vec::kLanes + i % Vec::kLanes;
   const bool ok = i < total && col < nvec;
   const size_t at = (size_t)row * nvec + col;
-  Vec16<kBF16> v;
-  if (ok) v.load(x + at * Vec16<kBF16>::N);
-  else v.zero();
-  const int p = scale_exponent(max8(v.amax()));
-  if (ok) store_stream(q + at, v.quantize(power_of_two(-p)));
-  if (i < total && (i & 7) == 0) scale[grp] = power_of_two(p);
+  Vec v = {v4u{0, 0, 0, 0}};
+  if (ok) v.v = load_stream(x + at);
+  const int p = scale_exponent(lanes_max<Vec::kLanes>(v.amax()));
+  if (ok) store_q(q + at * Vec::N, v.quantize(power_of_two(-p)));
+  if (i < total && i % Vec::kLanes == 0) scale[grp] = power_of_two(p);
 }
 
-// Blocks of 128 x 128: one thread block each, 64 elements a thread held in
-// registers between the maximum and the rounding, so x is read once.
+// Blocks of 128 x 128: one thread block each, its elements held in registers
+// between the maximum and the rounding, so x is read once.
 template <bool kBF16>
 __global__ __launch_bounds__(kBlock) void quantize_blocks_kernel(
     const v4u* __restrict__ x, uint32_t rows, uint32_t rblocks, uint32_t cblocks, uint32_t nvec,
-    v4u* __restrict__ q, float* __restrict__ scale) {
-  constexpr int kPass = kQuantBlock / (kBlock / 8);  // rows a thread holds
+    uint8_t* __restrict__ q, float* __restrict__ scale) {
+  typedef QuantVec<kBF16> Vec;
+  constexpr int kPer = kBlock / Vec::kLanes;    // rows a pass
+  constexpr int kPass = kQuantBlock / kPer;     // rows a thread holds
   __shared__ uint32_t part[kBlock / kWave];
   const uint32_t b = blockIdx.x;  // (batch, row block, column block)
   const uint32_t rb = b / cblocks, cb = b - rb * cblocks;
   const uint32_t batch = rb / rblocks, r0 = (rb - batch * rblocks) * kQuantBlock;
-  const uint32_t col = cb * 8 + (threadIdx.x & 7);
-  const uint32_t lr = threadIdx.x >> 3;
-  Vec16<kBF16> v[kPass];
+  const uint32_t col = cb * Vec::kLanes + threadIdx.x % Vec::kLanes;
+  const uint32_t lr = threadIdx.x / Vec::kLanes;
+  Vec v[kPass];
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < kPass; ++j) {
-    const uint32_t r = r0 + lr + j * (kBlock / 8);
-    if (col < nvec && r < rows)
-      v[j].load(x + (((size_t)batch * rows + r) * nvec + col) * Vec16<kBF16>::N);
-    else
-      v[j].zero();
+    const uint32_t r = r0 + lr + j * kPer;
+    v[j].v = v4u{0, 0, 0, 0};
+    if (col < nvec && r < rows) v[j].v = load_stream(x + ((size_t)batch * rows + r) * nvec + col);
   }
 #pragma unroll
   for (int j = 0; j < kPass; ++j) {
     const uint32_t a = v[j].amax();
     m = a > m ? a : m;
   }
-  m = group_reduce(m, kWave, [](uint32_t a, uint32_t c) { return a > c ? a : c; });
+  m = lanes_max<kWave>(m);
   if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = m;
   __syncthreads();
 #pragma unroll
@@ -76,41 +85,41 @@ __global__ __launch_bounds__(kBlock) void quantize_blocks_kernel(
   const float inv = power_of_two(-p);
 #pragma unroll
   for (int j = 0; j < kPass; ++j) {
-    const uint32_t r = r0 + lr + j * (kBlock / 8);
+    const uint32_t r = r0 + lr + j * kPer;
     if (col < nvec && r < rows)
-      store_stream(q + ((size_t)batch * rows + r) * nvec + col, v[j].quantize(inv));
+      store_q(q + (((size_t)batch * rows + r) * nvec + col) * Vec::N, v[j].quantize(inv));
   }
   if (threadIdx.x == 0) scale[b] = power_of_two(p);
 }
 
 // Dispatch: the lane layout of quantize_rows_kernel over x [T][H]; each lane
-// stores its 16 bytes to the token's k send rows (picks without a row inside
+// stores its bytes to the token's k send rows (picks without a row inside
 // [0, nrows) are skipped), the group's first lane the scale.
 template <bool kBF16, int KMAX>
 __global__ __launch_bounds__(kBlock) void dispatch_fp8_kernel(
     const v4u* __restrict__ x, const int32_t* __restrict__ pos, int k, uint32_t total,
-    uint32_t groups, uint32_t nvec, uint32_t nrows, v4u* __restrict__ q,
+    uint32_t groups, uint32_t nvec, uint32_t nrows, uint8_t* __restrict__ q,
     float* __restrict__ scale) {
+  typedef QuantVec<kBF16> Vec;
   const uint32_t i = blockIdx.x * (uint32_t)kBlock + threadIdx.x;
-  const uint32_t grp = i >> 3;
+  const uint32_t grp = i / Vec::kLanes;
   const uint32_t t = grp / groups, g = grp - t * groups;
-  const uint32_t col = g * 8 + (i & 7);
+  const uint32_t col = g * Vec::kLanes + i % Vec::kLanes;
   const bool live = i < total;
   const bool ok = live && col < nvec;
-  Vec16<kBF16> v;
-  if (ok) v.load(x + ((size_t)t * nvec + col) * Vec16<kBF16>::N);
-  else v.zero();
+  Vec v = {v4u{0, 0, 0, 0}};
+  if (ok) v.v = load_stream(x + (size_t)t * nvec + col);
   int32_t P[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) P[j] = (live && j < k) ? pos[(size_t)t * k + j] : -1;
-  const int p = scale_exponent(max8(v.amax()));
-  const v4u out = v.quantize(power_of_two(-p));
+  const int p = scale_exponent(lanes_max<Vec::kLanes>(v.amax()));
+  const typename Vec::Out out = v.quantize(power_of_two(-p));
   const float s = power_of_two(p);
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
     if ((uint32_t)P[j] < nrows) {
-      if (ok) store_stream(q + (size_t)P[j] * nvec + col, out);
-      if ((i & 7) == 0) scale[(size_t)P[j] * groups + g] = s;
+      if (ok) store_q(q + ((size_t)P[j] * nvec + col) * Vec::N, out);
+      if (i % Vec::kLanes == 0) scale[(size_t)P[j] * groups + g] = s;
     }
   }
 }
@@ -120,12 +129,13 @@ __global__ __launch_bounds__(kBlock) void dispatch_fp8_kernel(
 hipError_t launch_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int cols,
                            int block_rows, void* q, float* scale, hipStream_t s) {
   if (batch == 0 || rows == 0) return hipSuccess;
-  const uint32_t nvec = (uint32_t)(cols / 16);
+  const int per_vec = dtype == MOE_BF16 ? 8 : 4;  // elements of a 16-byte vector
+  const uint32_t nvec = (uint32_t)(cols / per_vec);
   const uint32_t groups = (uint32_t)((cols + kQuantBlock - 1) / kQuantBlock);
   const v4u* xv = static_cast<const v4u*>(x);
-  v4u* qv = static_cast<v4u*>(q);
+  uint8_t* qv = static_cast<uint8_t*>(q);
   if (block_rows == 1) {
-    const uint32_t total = (uint32_t)(batch * rows * groups * 8);
+    const uint32_t total = (uint32_t)(batch * rows * groups * (kQuantBlock / per_vec));
     const dim3 grid((total + kBlock - 1) / kBlock);
     return dtype == MOE_BF16 ? launch(quantize_rows_kernel<true>, grid, dim3(kBlock), 0, s, xv,
                                       total, groups, nvec, qv, scale)
@@ -143,15 +153,16 @@ hipError_t launch_quantize(const void* x, int dtype, int64_t batch, int64_t rows
 hipError_t launch_dispatch_fp8(const void* x, int dtype, const int32_t* pos, int T, int k, int H,
                                int64_t send_rows, void* send_q, float* send_scale, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const uint32_t nvec = (uint32_t)(H / 16);
+  const int per_vec = dtype == MOE_BF16 ? 8 : 4;
+  const uint32_t nvec = (uint32_t)(H / per_vec);
   const uint32_t groups = (uint32_t)((H + kQuantBlock - 1) / kQuantBlock);
-  const uint32_t total = (uint32_t)T * groups * 8;
+  const uint32_t total = (uint32_t)T * groups * (kQuantBlock / per_vec);
   const dim3 grid((total + kBlock - 1) / kBlock);
   auto go = [&](auto kmax) {
     constexpr int KM = decltype(kmax)::value;
     auto run = [&](auto kernel) {
       return launch(kernel, grid, dim3(kBlock), 0, s, static_cast<const v4u*>(x), pos, k, total,
-                    groups, nvec, (uint32_t)send_rows, static_cast<v4u*>(send_q), send_scale);
+                    groups, nvec, (uint32_t)send_rows, static_cast<uint8_t*>(send_q), send_scale);
     };
     return dtype == MOE_BF16 ? run(dispatch_fp8_kernel<true, KM>)
                              : run(dispatch_fp8_kernel<false, KM>);

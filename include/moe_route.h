@@ -331,8 +331,8 @@ int moe_expert_swiglu(const moe_shape* shape, int32_t I, const void* send_buf,
  * magnitude, scale = 2^p with the smallest p >= -126 for which amax <= 448 * 2^p
  * (1 when amax is 0), q = x * 2^-p rounded once to e4m3 (nearest, ties to even);
  * infinities saturate to +-448, NaN stays NaN.
- * cols % 16 == 0; batch * rows * 8 * ceil(cols/128) < 2^31; x and q 16-byte
- * aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also cols % 16),
+ * cols % 16 == 0; batch * rows * ceil(cols/128) < 2^27 for bf16, 2^26 for fp32; x and
+ * q 16-byte aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also cols % 16),
  * MOE_ERR_UNSUPPORTED (dtype), MOE_ERR_DEVICE. */
 int moe_quantize(const void* x, int32_t dtype, int32_t batch, int32_t rows, int32_t cols,
                  int32_t block_rows, void* q, float* scale, moe_stream_t stream);
