@@ -104,12 +104,16 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Block tiles of BM x BN by WM x WN waves, each wave (BM/WM) x (BN/WN) as MI x NI
-// fragments of 16 x 16. N: rows of one expert's B (2 I for gate/up). One block a
-// compute unit; it takes every gridDim.x / 8-th tile of its XCD's share of the
-// list (contiguous, so the XCD's L2 serves its rows and weights), and the K steps of its
-// tiles are one stream: the loads run two steps ahead, into the next tile's first
-// steps while this one's last run and its results are stored.
+// Block tiles of BM x BN by WM x WN waves, each wave BM/WM x BN/WN as MI x NI
+// fragments of 16 x 16; the wave's row fragments are 16 WM rows apart, so the waves
+// share the rows of a partial tile evenly, and tiles of up to a quarter or a half of
+// the rows run with one or two fragments a wave. N: rows of one expert's B (2 I
+// for gate/up). One block a compute unit; it takes every gridDim.x / 8-th tile of
+// its XCD's share of the list (contiguous, so the XCD's L2 serves its rows and
+// weights), and the K steps of its tiles are one stream: the loads run two steps
+// ahead, into the next tile's first steps while this one's last run and its results are
+// stored. The tiles of an XCD's last, partial round are cut into two or four by
+// rows where that still gives each unit one.
 template <bool kGateUp, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ Asc,
@@ -142,13 +146,25 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   const int total = __builtin_amdgcn_readfirstlane(pre[E]) * ntiles;
   const int per = (total + kXCD - 1) / kXCD;
   const int hop = gridDim.x / kXCD;
-  const int xcd = blockIdx.x % kXCD;
-  const int limit = (xcd + 1) * per < total ? (xcd + 1) * per : total;
-  int place = xcd * per + blockIdx.x / kXCD;
-  if (place >= limit) return;  // uniform over the block
+  const int first = blockIdx.x % kXCD * per;
+  const int mine = total - first < per ? total - first : per;  // the XCD's tiles
+  const int whole = mine > 0 ? mine / hop * hop : 0, rest = mine - whole;
+  const int cut = rest * 4 <= hop ? 4 : (rest * 2 <= hop ? 2 : 1);
+  const int limit = whole + rest * cut;
+  int place = blockIdx.x / kXCD;
+  if (mine <= 0 || place >= limit) return;  // uniform over the block
   const auto tile_of = [&](int p) {
     if (p >= limit) return Tile{-1, 0, 0, 0};
-    return tile_at_place<BM>(pre, offs, cnts, E, rows_total, ntiles, p);
+    const int q = p - whole;  // past the whole rounds: part q % cut of a tile
+    Tile t = tile_at_place<BM>(pre, offs, cnts, E, rows_total, ntiles,
+                               first + (q < 0 ? p : whole + q / cut));
+    if (q >= 0 && cut > 1 && t.e >= 0) {
+      const int r0 = q % cut * (BM / cut), left = t.rows - r0;
+      t.rows = left < BM / cut ? left : BM / cut;
+      t.row0 += r0;
+      if (left <= 0) t = {-1, 0, 0, 0};
+    }
+    return t;
   };
 
   // ---- loads: one wave instruction fills eight 128-byte tile rows, lane l the
@@ -219,7 +235,7 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   // bit 0 keep those apart; in bit 1 (2 (l / 16) and the next) half the LDS
   // cycles were bank conflicts.
   const int fi = lane & 15, fc = lane >> 4;
-  const int arow = wm * (BM / WM) + fi;
+  const int arow = wm * 16 + fi;  // of fragment 0; the others 16 WM rows apart
   const int a0 = arow * kBK + ((fc ^ a_key(arow)) << 4);
   const int a1 = arow * kBK + (((fc + 4) ^ a_key(arow)) << 4);
   const int brow = (kGateUp ? wn * (NO / WN) : wn * (BN / WN)) + 8 * (fi >> 2) + (fi & 3);
@@ -230,7 +246,8 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
     const i32x4 hi = *reinterpret_cast<const i32x4*>(st + o1 + off);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  auto read_a = [&](const uint8_t* st, int mi) { return frag(st, a0, a1, mi * 16 * kBK); };
+  constexpr int kFragRows = 16 * WM;
+  auto read_a = [&](const uint8_t* st, int mi) { return frag(st, a0, a1, mi * kFragRows * kBK); };
   auto read_b = [&](const uint8_t* st, int ni) {
     // rows of fragment ni past this wave's first: pairs of 32, four apart inside
     const int q = kGateUp ? ni % (NI / 2) : ni;
@@ -238,17 +255,15 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
     return frag(st, b0, b1, r * kBK);
   };
   auto read_s = [&](const uint8_t* st, int mi) -> float {
-    return *reinterpret_cast<const float*>(st + (BM + BN) * kBK + (arow + mi * 16) * 4);
+    return *reinterpret_cast<const float*>(st + (BM + BN) * kBK + (arow + mi * kFragRows) * 4);
   };
 
   // ---- the tile being computed
   Tile tile = tile_of(place);
-  bool live;            // this wave has rows in it: the others only load and meet the barriers
   int ncol;             // first output column of the wave
   const float *bs0, *bs1;  // weight scales of its column block(s), one a K step
   auto enter = [&](const Tile& t) __attribute__((always_inline)) {
     tile = t;
-    live = wm * (BM / WM) < t.rows;
     ncol = t.ntile * NO + wn * (NO / WN);
     const int nb = ncol / kQuantBlock < NB ? ncol / kQuantBlock : NB - 1;
     bs0 = Bsc + ((int64_t)(t.e < 0 ? 0 : t.e) * NB + nb) * KB;
@@ -259,20 +274,20 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   f32x4 acc[NI][MI];
   i32x8 fa[MI], fb[4];
   float sa[MI];
-  auto clear = [&]() __attribute__((always_inline)) {
+  // ML: the wave's row fragments in use
+  auto first_frags = [&](auto ml, const uint8_t* st) __attribute__((always_inline)) {
+    constexpr int ML = decltype(ml)::value;
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) acc[ni][mi] = f32x4{0, 0, 0, 0};
-  };
-  auto first_frags = [&](const uint8_t* st) __attribute__((always_inline)) {
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
+    for (int mi = 0; mi < ML; ++mi) {
       fa[mi] = read_a(st, mi);
       sa[mi] = read_s(st, mi);
     }
     fb[0] = read_b(st, 0);
     fb[1] = read_b(st, 1);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+      for (int mi = 0; mi < ML; ++mi) acc[ni][mi] = f32x4{0, 0, 0, 0};
   };
 
   // A step reads stage S. Its fragments of A, the row scales and the first two
@@ -288,20 +303,21 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   // raised for the columns before the barrier (gate/up 455 against 415 us, also because the
   // scheduling fence keeps the registers from spilling).
   constexpr int kAfter = 5;
-  auto step = [&](auto S, int kt) __attribute__((always_inline)) {
+  auto step = [&](auto ml, auto S, int kt) __attribute__((always_inline)) {
+    constexpr int ML = decltype(ml)::value;
     uint8_t* cur = stage(S);
     uint8_t* nxt = stage(std::integral_constant<int, decltype(S)::value + 1>{});
     const float w0 = bs0[kt], w1 = bs1[kt];
-    float s0[MI], s1[MI];
+    float s0[ML], s1[ML];
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
+    for (int mi = 0; mi < ML; ++mi) {
       s0[mi] = sa[mi] * w0;
       s1[mi] = kGateUp ? sa[mi] * w1 : s0[mi];
     }
     constexpr int kRing = 4, kLag = 2;                      // results in flight
-    constexpr int kBefore = (NI - 2) * MI, kAll = NI * MI;  // MFMAs before the barrier, in all
-    auto ni_of = [](int j) { return j < kBefore ? j / MI : NI - 2 + (j - kBefore) % 2; };
-    auto mi_of = [](int j) { return j < kBefore ? j % MI : (j - kBefore) / 2; };
+    constexpr int kBefore = (NI - 2) * ML, kAll = NI * ML;  // MFMAs before the barrier, in all
+    auto ni_of = [](int j) { return j < kBefore ? j / ML : NI - 2 + (j - kBefore) % 2; };
+    auto mi_of = [](int j) { return j < kBefore ? j % ML : (j - kBefore) / 2; };
     f32x4 t[kRing];
     auto fold = [&](int j) __attribute__((always_inline)) {
       const int ni = ni_of(j), mi = mi_of(j);
@@ -319,44 +335,38 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
     for (int ni = 0; ni < NI - 2; ++ni) {
       fb[(ni + 2) % 4] = read_b(cur, ni + 2);
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        const int j = ni * MI + mi, q = kAfter + j / 2;
+      for (int mi = 0; mi < ML; ++mi) {
+        const int j = ni * ML + mi, q = kAfter + j / 2;
         mma(j);
         if (j % 2 == 0 && q < kLoads) issue(nxt, q);
       }
     }
     __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+    for (int q = kAfter + (kBefore + 1) / 2; q < kLoads; ++q) issue(nxt, q);  // with few MFMAs
     next_load();
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
     __syncthreads();
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
+    for (int mi = 0; mi < ML; ++mi) {
       mma(kBefore + 2 * mi);
       mma(kBefore + 2 * mi + 1);
 #pragma unroll
       for (int q = 0; q < kAfter; ++q)
-        if (q * MI / kAfter == mi) issue(cur, q);
+        if (q * ML / kAfter == mi) issue(cur, q);
       fa[mi] = read_a(nxt, mi);
       sa[mi] = read_s(nxt, mi);
       if (mi < 2) fb[mi] = read_b(nxt, mi);
+      if (ML == 1) fb[1] = read_b(nxt, 1);
     }
 #pragma unroll
     for (int j = kAll - kLag; j < kAll; ++j) fold(j);
   };
-  // The same loads and barrier of a wave without rows in the tile.
-  auto dead_step = [&](uint8_t* cur, uint8_t* nxt) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = kAfter; q < kLoads; ++q) issue(nxt, q);
-    next_load();
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kAfter; ++q) issue(cur, q);
-  };
 
   // ---- results: the stores go through descriptors over the tile's rows, whose
   // range check drops the rows past the last one.
-  auto finish = [&]() __attribute__((always_inline)) {
+  auto finish = [&](auto ml) __attribute__((always_inline)) {
+    constexpr int ML = decltype(ml)::value;
     const int g = lane >> 4;
     if constexpr (!kGateUp) {
       const __amdgpu_buffer_rsrc_t crsrc = make_rsrc(
@@ -365,12 +375,12 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
       for (int p = 0; p < NI / 2; ++p) {
         const int n = ncol + 32 * p + 8 * g;
 #pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
+        for (int mi = 0; mi < ML; ++mi) {
           const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
           const v4u v = {bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]),
                          bf16x2_rne(hi[0], hi[1]), bf16x2_rne(hi[2], hi[3])};
           // columns past N would wrap into the next row: offset out of range instead
-          const uint32_t off = n < N ? ((uint32_t)(arow + mi * 16) * (uint32_t)N + n) * 2 : kOutside;
+          const uint32_t off = n < N ? ((uint32_t)(arow + mi * kFragRows) * (uint32_t)N + n) * 2 : kOutside;
           __builtin_amdgcn_raw_buffer_store_b128(v, crsrc, off, 0, 0);
         }
       }
@@ -380,7 +390,7 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
       // waves' through LDS. Rows are whole scale blocks of h.
       {
 #pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
+        for (int mi = 0; mi < ML; ++mi) {
           uint32_t m = 0;
 #pragma unroll
           for (int ni = 0; ni < NI / 2; ++ni)
@@ -395,7 +405,7 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
           m = o > m ? o : m;
           o = (uint32_t)__shfl_xor((int)m, 32);
           m = o > m ? o : m;
-          if (g == 0) ex[wn * BM + arow + mi * 16] = m;
+          if (g == 0) ex[wn * BM + arow + mi * kFragRows] = m;
         }
       }
       lds_barrier();  // the maxima are read before the next step's barrier, so before they change
@@ -403,8 +413,8 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
           make_rsrc(static_cast<uint8_t*>(C) + (int64_t)tile.row0 * I, (int64_t)tile.rows * I);
       const int IB = I / kQuantBlock;
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        const int m = arow + mi * 16;
+      for (int mi = 0; mi < ML; ++mi) {
+        const int m = arow + mi * kFragRows;
         uint32_t a = 0;
 #pragma unroll
         for (int w = 0; w < WN; ++w) a = ex[w * BM + m] > a ? ex[w * BM + m] : a;
@@ -441,27 +451,23 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   for (int par = 0;;) {
     const Tile ahead = tile_of(place + hop);
     after = source_of(ahead);
-    if (live) {
-      clear();
-      first_frags(par ? lds1 : lds0);
+    auto compute = [&](auto ml) __attribute__((always_inline)) {
+      first_frags(ml, par ? lds1 : lds0);
       int kt = 0;
-      if (par) step(I1{}, kt++);
+      if (par) step(ml, I1{}, kt++);
       for (; kt + 2 <= KB; kt += 2) {
-        step(I0{}, kt);
-        step(I1{}, kt + 1);
+        step(ml, I0{}, kt);
+        step(ml, I1{}, kt + 1);
       }
-      if (kt < KB) step(I0{}, kt);
+      if (kt < KB) step(ml, I0{}, kt);
       // The loads that run ahead land here, where it costs the least: past this point
       // nothing is pending in either stage, whichever the next tile begins with.
       __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-      finish();
-    } else {
-      for (int kt = 0; kt < KB; ++kt) {
-        if ((kt + par) & 1) dead_step(lds1, lds0);
-        else dead_step(lds0, lds1);
-      }
-      if constexpr (kGateUp) lds_barrier();  // the one in finish()
-    }
+      finish(ml);
+    };
+    if (tile.rows > BM / 2) compute(std::integral_constant<int, MI>{});
+    else if (tile.rows > BM / 4) compute(std::integral_constant<int, MI / 2>{});
+    else compute(std::integral_constant<int, MI / 4>{});
     par = (par + KB) & 1;
     place += hop;
     if (place >= limit) break;
@@ -480,8 +486,9 @@ hipError_t run_gemm(const void* a, const float* asc, int64_t rows, int E, const 
   const int ntiles = (cols + NO - 1) / NO;
   // every expert with rows adds at most one partial m-tile
   const int64_t mt = rows / BM + (rows < E ? rows : E);
-  int64_t per = (mt * ntiles + kXCD - 1) / kXCD;
-  if (per > kUnitsPerXcd) per = kUnitsPerXcd;  // one block a compute unit
+  // one block a compute unit (a tile alone on its XCD is cut into four)
+  int64_t per = 4 * ((mt * ntiles + kXCD - 1) / kXCD);
+  if (per > kUnitsPerXcd) per = kUnitsPerXcd;
   return launch(gemm_fp8_kernel<kGateUp, BM, BN, WM, WN>, dim3((unsigned)(per * kXCD)),
                 dim3(kWave * WM * WN), 0, s, static_cast<const uint8_t*>(a), asc, offs, cnts, E,
                 rows, static_cast<const uint8_t*>(w), wsc, N, K, c, csc, ntiles);

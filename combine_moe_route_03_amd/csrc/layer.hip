@@ -33,6 +33,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kMaxPicks = 1024;
 constexpr int kMaxE = 1024;
 constexpr int kRouteT = 8;     // most tokens that every gate/up block routes itself
+constexpr uint32_t kLdsBytes = 160 * 1024;  // of a compute unit
 constexpr int kUpWaves = 4;    // waves of a gate/up block
 constexpr int kUpCols = 8;     // intermediate columns of a unit (8 gate + 8 up rows)
 
@@ -180,13 +181,15 @@ constexpr int kRing = kFp8 ? (NB == 1 ? (RW == 8 ? 6 : 4) : (NB == 2 ? 3 : 2))
 // acc[t] += the products of the unit's rows with NB x 8 tokens over n K steps
 // from s0, beginning with step s0 + rot. woff: byte offsets in wb of the lane's two rows at
 // its chunk (RW = 8: the first only), wrow their LDS rows; xoff[b]: in xb of
-// its token of group b at its chunk (kOutside without a token); c0, c1 (e4m3): in cb of the scales of D registers 0-1 and 2-3, one a
-// step.
+// its token of group b at its chunk (kOutside without a token); c0, c1 (e4m3): scales of D registers 0-1 and 2-3, one
+// a step (uniform: scalar loads; through the vector path they were two of six
+// load instructions a step).
 template <bool kFp8, int RW, int NB, int D>
 __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
                                           const uint32_t (&woff)[2], const int (&wrow)[2],
                                           const Buffer& xb, const uint32_t (&xoff)[NB],
-                                          const Buffer& cb, uint32_t c0, uint32_t c1,
+                                          const float* __restrict__ c0,
+                                          const float* __restrict__ c1,
                                           int s0, int n, int rot, f32x4 (&acc)[(NB + 1) / 2]) {
   constexpr int kB = Step<kFp8>::kB, NTL = (NB + 1) / 2, RI = RW / 8;
   const int lane = threadIdx.x & (kWave - 1);
@@ -206,8 +209,8 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
       for (int p = 0; p < kB; ++p)
         x[u][b][p] = load16(xb.at(in), xoff[b], s * (Step<kFp8>::kCols * 2) + 128 * p);
     if constexpr (kFp8) {
-      a0[u] = load4(cb.at(in), c0, s * 4);
-      a1[u] = load4(cb.at(in), c1, s * 4);
+      a0[u] = c0[in ? s : (uint32_t)s0];
+      a1[u] = c1[in ? s : (uint32_t)s0];
     }
   };
   uint8_t* xs = stage + 2048;
@@ -328,13 +331,10 @@ __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void 
   const int steps = H / Step<kFp8>::kCols;
   const int s0 = steps * ks / KS, n = steps * (ks + 1) / KS - s0;
   const int rot = n > 0 ? (int)(blockIdx.x + slot) * 5 % n : 0;  // alike in a block: x from L1
-  Buffer cb = xb;
-  uint32_t c0 = 0, c1 = 0;
+  const float *c0 = nullptr, *c1 = nullptr;
   if constexpr (kFp8) {
-    const int nb = 2 * I / kQuantBlock;
-    cb = {wsc + (int64_t)e * nb * steps, (uint32_t)nb * steps * 4};
-    c0 = (uint32_t)(j0 / kQuantBlock) * steps * 4;
-    c1 = c0 + (uint32_t)(I / kQuantBlock) * steps * 4;
+    c0 = wsc + ((int64_t)e * (2 * I / kQuantBlock) + j0 / kQuantBlock) * steps;
+    c1 = c0 + (int64_t)(I / kQuantBlock) * steps;
   }
   auto pass = [&](auto nb_) __attribute__((always_inline)) {
     constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void 
     }
 #pragma unroll
     for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
-    dot_steps<kFp8, 16, NB, kRing<kFp8, 16, NB>>(stage[wid], wb, woff, wrow, xb, xoff, cb, c0, c1, s0,
+    dot_steps<kFp8, 16, NB, kRing<kFp8, 16, NB>>(stage[wid], wb, woff, wrow, xb, xoff, c0, c1, s0,
                                              n, rot, acc);
     if constexpr (KS > 1) {
 #pragma unroll
@@ -441,13 +441,9 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
     if (cnt <= 0) continue;                           // three groups of four
     const uint16_t* pick = pk + slot_first(word) + grp * kGroup;
     const Buffer wb = {w + (int64_t)e * H * I * kWB, (uint32_t)H * (uint32_t)(I * kWB)};
-    Buffer cb = hb;
-    uint32_t sc = 0;
-    if constexpr (kFp8) {
-      const int nb = H / kQuantBlock;
-      cb = {wsc + (int64_t)e * nb * steps, (uint32_t)nb * steps * 4};
-      sc = (uint32_t)(c0 / kQuantBlock) * steps * 4;
-    }
+    const float* sc = nullptr;
+    if constexpr (kFp8)
+      sc = wsc + ((int64_t)e * (H / kQuantBlock) + c0 / kQuantBlock) * steps;
     auto pass = [&](auto nb_) __attribute__((always_inline)) {
       constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
       uint32_t hoff[NB];
@@ -460,7 +456,7 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
 #pragma unroll
       for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
       dot_steps<kFp8, RW, NB, kRing<kFp8, RW, NB>>(stage + wid * stage_bytes(kMaxNB), wb, woff, wrow,
-                                                hb, hoff, cb, sc, sc, s0, s1 - s0, rot, acc);
+                                                hb, hoff, sc, sc, s0, s1 - s0, rot, acc);
 #pragma unroll
       for (int t = 0; t < NTL; ++t) {
         const int c = 16 * t + i;
@@ -572,6 +568,7 @@ hipError_t run_layer(const float* logits, const void* x, int T, int H, int E, in
     using I8 = std::integral_constant<int, 8>;
     using I16 = std::integral_constant<int, 16>;
     if (T <= 8) return down(rw, I1{}, I16{});
+    if (decltype(rw)::value == 8 && lds(8, 4, 16) <= kLdsBytes) return down(rw, I4{}, I16{});
     return down(rw, I4{}, I8{});
   };
   // 16 columns a block where that makes a block for every compute unit
