@@ -29,11 +29,12 @@ struct Tile {
   int e, row0, rows, ntile;  // e < 0: no tile for this block
 };
 
-// Block -> tile. The tiles of all experts, in patches of kGroupM m-tiles by all
-// n-tiles, form one list; workgroups are dealt to the 8 XCDs round-robin and
-// each XCD takes one contiguous share of the list, so it reads its rows and
-// weights through its own L2 (a list of tiles rather than of m-tiles, so that
-// one expert's few rows still spread over all XCDs). Counts that leave [0,
+// Block -> tile, for tiles that share weights with their neighbours at most. The
+// tiles of all experts, in patches of kGroupM m-tiles by all n-tiles, form one list;
+// workgroups are dealt to the 8 XCDs round-robin and each XCD takes every eighth
+// run of kGroupM tiles: the m-tiles of a long expert read the same weights through
+// one L2, and the long experts' tiles, which take longer, spread over the XCDs
+// (contiguous shares: decode product with hot experts 243 us). Counts that leave [0,
 // rows_total) give no tile. Called by the whole block; info: 4 ints of LDS.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offs,
@@ -57,10 +58,9 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offs,
     }
     const int MT = __shfl(incl, kWave - 1);
     const int total = MT * ntiles;
-    const int per = (total + kXCD - 1) / kXCD;
     const int slot = blockIdx.x / kXCD;
-    const int lin = (blockIdx.x % kXCD) * per + slot;
-    if (slot < per && lin < total) {
+    const int lin = ((slot / kGroupM) * kXCD + blockIdx.x % kXCD) * kGroupM + slot % kGroupM;
+    if (lin < total) {
       const int grp = lin / (kGroupM * ntiles), r = lin - grp * kGroupM * ntiles;
       const int gh = MT - grp * kGroupM < kGroupM ? MT - grp * kGroupM : kGroupM;
       const int ntile = r / gh, mt = grp * kGroupM + (r - ntile * gh);

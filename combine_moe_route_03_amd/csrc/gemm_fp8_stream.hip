@@ -248,9 +248,9 @@ hipError_t run(const void* a, const float* asc, int64_t rows, int E, const int32
   constexpr int kNO = kWaves * (kGateUp ? 16 : 32);
   const int ntiles = (cols + kNO - 1) / kNO;
   const int64_t mt = rows / kRows + (rows < E ? rows : E);
-  const int64_t per = (mt * ntiles + kXCD - 1) / kXCD;
-  return launch(gemm_fp8_stream_kernel<kGateUp>, dim3((unsigned)(per * kXCD)), dim3(kWave * kWaves),
-                0, s, static_cast<const uint8_t*>(a), asc, offs, cnts, E, rows,
+  const int64_t runs = (mt * ntiles + kGroupM * kXCD - 1) / (kGroupM * kXCD);
+  return launch(gemm_fp8_stream_kernel<kGateUp>, dim3((unsigned)(runs * kGroupM * kXCD)),
+                dim3(kWave * kWaves), 0, s, static_cast<const uint8_t*>(a), asc, offs, cnts, E, rows,
                 static_cast<const uint8_t*>(w), wsc, N, K, c, csc, ntiles);
 }
 
