@@ -193,6 +193,23 @@ def test_expert_gemm_fp8_nan_stays_in_its_row():
     assert bool(out[17].isnan().all()) and torch.equal(out[keep], clean[keep])
 
 
+def test_without_rows():
+    """No tokens: every entry returns empty outputs and touches nothing."""
+    shape = moe.Shape(0, 256, 4, 2, 1, 1, torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32, device=DEV)
+    q, s = moe.dispatch_copy_fp8(torch.empty(0, 256, dtype=torch.bfloat16, device=DEV),
+                                 torch.empty(0, 2, dtype=torch.int32, device=DEV), shape)
+    (wg, sg), (wd, sd) = [[t.to(DEV) for t in fp8_weights(4, *nk, 2)] for nk in ((256, 256), (256, 128))]
+    assert moe.expert_gemm_fp8(q, s, i, i, wg, sg).shape == (0, 256)
+    assert moe.expert_swiglu_fp8(q, s, i, i, shape, wg, sg, wd, sd).shape == (0, 256)
+    # rows, but no expert has any
+    a, sa = moe.quantize(torch.ones(300, 256, device=DEV))
+    out = torch.full((300, 256), 4.0, dtype=torch.bfloat16, device=DEV)
+    moe.expert_gemm_fp8(a, sa, i, i, wg, sg, out=out)
+    moe.expert_gemm_fp8(a[:8], sa[:8], i, i, wg, sg, out=out[:8])
+    assert bool((out == 4.0).all())
+
+
 # ------------------------------------------------------------------ FFN
 
 @pytest.mark.parametrize("counts,H,I", [
