@@ -47,7 +47,7 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offs,
     const int e0 = lane * c, e1 = (e0 + c < E) ? e0 + c : E;
     const auto mtiles = [&](int e) {
       const int n = cnts[e];
-      return n > 0 && n <= rows_total ? (n + BM - 1) / BM : 0;
+      return n > 0 && n <= rows_total ? (n - 1) / BM + 1 : 0;
     };
     int mine = 0;
     for (int e = e0; e < e1; ++e) mine += mtiles(e);

@@ -50,7 +50,9 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* lds
 }
 
 // m-tile prefix sums of the experts in LDS: pre[e] m-tiles before expert e, pre[E] in
-// all. Counts outside [0, rows_total] give no tile. Called by the whole block.
+// all. Counts outside [0, rows_total] give no tile, and the list ends with as many
+// tiles as buckets that do not overlap can have, so that any counts make a
+// bounded list. Called by the whole block.
 template <int BM>
 __device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ cnts, int E,
                                             int64_t rows_total, int* pre) {
@@ -58,18 +60,23 @@ __device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ cnts, in
     const int lane = threadIdx.x;
     const int c = (E + kWave - 1) / kWave;  // lane l scans experts [l*c, l*c + c)
     const int e0 = lane * c, e1 = (e0 + c < E) ? e0 + c : E;
+    const int most = (int)(rows_total / BM + (rows_total < E ? rows_total : E));
     int mine = 0;
     for (int e = e0; e < e1; ++e) {
       const int n = cnts[e];
-      mine += n > 0 && n <= rows_total ? (n + BM - 1) / BM : 0;
+      mine += n > 0 && n <= rows_total ? (n - 1) / BM + 1 : 0;
       pre[e + 1] = mine;
     }
+    mine = mine < most ? mine : most;
     int incl = mine;
     for (int o = 1; o < kWave; o <<= 1) {
       const int y = __shfl_up(incl, o);
       if (lane >= o) incl += y;
     }
-    for (int e = e0; e < e1; ++e) pre[e + 1] += incl - mine;
+    for (int e = e0; e < e1; ++e) {
+      const int p = pre[e + 1] + incl - mine;
+      pre[e + 1] = p < most ? p : most;
+    }
     if (lane == 0) pre[0] = 0;
   }
   __syncthreads();

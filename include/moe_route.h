@@ -353,8 +353,9 @@ int moe_dispatch_copy_fp8(const moe_shape* shape, const void* x, const int32_t* 
  * untouched. Each 128-column product and the sum over b are held in fp32; the
  * matrix instruction drops, of each run of 8 products, what lies below 2^-13 of
  * the run's largest (a result is off by at most 2^-10 of the sum of magnitudes,
- * and on average by far less than its rounding to bf16). A dense product is E = 1 with offsets {0} and counts {rows}. Buckets (of any
- * order) that do not lie in [0, rows) give no output.
+ * and on average by far less than its rounding to bf16). A dense product is E = 1
+ * with offsets {0} and counts {rows}. Buckets may lie in any order and do not
+ * overlap; one that does not lie in [0, rows) gives no output.
  * a [rows][K], w [E][N][K] e4m3, a_scale [rows][K/128], w_scale
  * [E][ceil(N/128)][K/128] fp32, out [rows][N] bf16. K % 128 == 0, N % 16 == 0,
  * 1 <= E <= 1024, N*K < 2^31, 256*K < 2^31, 512*N < 2^31; a, w, out 16-byte aligned.
@@ -400,7 +401,9 @@ size_t moe_layer_workspace_bytes(const moe_shape* shape, int32_t I);
  * all sums in fp32 (finite operands as in moe_expert_swiglu). Differs from
  * moe_route + moe_dispatch + moe_expert_swiglu + moe_combine in that the
  * experts' outputs are not rounded to bf16 before they are weighted. Only live
- * experts' weights are read, once (again for every further 64 picks of an expert).
+ * experts' weights are read, once (w_down again for every further 32 picks of an
+ * expert). Two launches for T <= 8, else one more to route and one more again
+ * where a block cannot route all tokens at a time.
  * weight_dtype MOE_BF16: w_gate_up [E][2I][H], w_down [E][H][I] bf16, the scales
  * unused (NULL). MOE_F8E4M3: the same in e4m3 with s_gate_up [E][2I/128][H/128],
  * s_down [E][H/128][I/128] fp32; the tokens stay bf16.

@@ -182,6 +182,34 @@ def test_expert_gemm_fp8_buckets_outside_the_rows_are_ignored():
     assert bool((out[4:] == 3.0).all()) and not bool((out[:4] == 3.0).all())
 
 
+def test_expert_gemm_fp8_bad_buckets_among_many_rows():
+    """The same with more rows than 24 an expert: counts and offsets that leave the rows."""
+    c = torch.tensor([130, 100, 7, 5000], dtype=torch.int32, device=DEV)
+    o = torch.tensor([10, 250, -2, 0], dtype=torch.int32, device=DEV)  # only the first lies inside
+    a, sa = moe.quantize(randn(300, 256, seed=1).to(DEV))
+    w, sw = [t.to(DEV) for t in fp8_weights(4, 64, 256, 2)]
+    out = torch.full((300, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    moe.expert_gemm_fp8(a, sa, o, c, w, sw, out=out)
+    assert bool((out[:10] == 3.0).all()) and bool((out[140:] == 3.0).all())
+    o[1:], c[1:] = 0, 0
+    only = torch.full_like(out, 3.0)
+    moe.expert_gemm_fp8(a, sa, o, c, w, sw, out=only)
+    assert torch.equal(out, only) and not bool((out[10:140] == 3.0).all())
+
+
+@pytest.mark.parametrize("rows", [20, 600])
+def test_expert_gemm_fp8_counts_beyond_the_rows_end(rows):
+    """Every expert claims all rows (no routing does): the list of tiles stays as long as
+    that of buckets that do not overlap, and what is written is an expert's product."""
+    E = 5
+    a, sa = moe.quantize(randn(rows, 256, seed=1).to(DEV))
+    w, sw = [t.to(DEV).expand(E, -1, -1).contiguous() for t in fp8_weights(1, 64, 256, 2)]
+    o, c = (torch.full((E,), v, dtype=torch.int32, device=DEV) for v in (0, rows))
+    out = moe.expert_gemm_fp8(a, sa, o, c, w, sw)
+    one = moe.expert_gemm_fp8(a, sa, o[:1], c[:1], w[:1], sw[:1])
+    assert torch.equal(out, one)
+
+
 def test_expert_gemm_fp8_nan_stays_in_its_row():
     a, sa = moe.quantize(randn(40, 256, seed=1).to(DEV))
     clean = moe.expert_gemm_fp8(a, sa, *[t.to(DEV) for t in buckets([40])[1::-1]],
