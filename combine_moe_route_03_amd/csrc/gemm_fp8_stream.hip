@@ -4,7 +4,11 @@
 // (stream.h) instead of through tiles shared by a block, and a block takes up to
 // 32 rows of an expert. An expert with more rows is several row tiles, adjacent
 // in the tile list, so they run at one time on one XCD and the weights come from
-// its L2.
+// its L2: those tiles load them cached, all others past the caches (128 experts, N
+// 2816, K 4096, 128 tokens most of whose picks go to 8 experts: 243 us with every
+// load past the caches, 211 with the cached ones for 17 to 32 rows of any expert,
+// 198 = 6.2 TB/s as it is, 6.3 TB/s with even routing; memory reads 1.48, 1.37 and
+// 1.33 GB for 1.23 GB of weights).
 //
 // A wave computes 32 weight rows by up to 32 tokens (two fragments of 16 rows, so
 // that a token fragment is loaded once for both), one
@@ -40,7 +44,8 @@ constexpr int kRing = NB == 4 ? 2 : 3;
 // chunk, wrow their LDS rows in the fragment; xoff[b]: in xb of its token of
 // group b at its chunk (kOutside: none); ss: row scales [kRows][kSPitch] of these
 // steps; c0, c1: weight scales of D registers 0-1 and 2-3, lane l's of step s0 + l.
-template <bool kTwoScales, int NB>
+// kShared: other blocks read these weights.
+template <bool kTwoScales, int NB, bool kShared>
 __device__ __forceinline__ void dot_steps8(uint8_t* stage, const Buffer& wb,
                                            const uint32_t (&woff)[4], const int (&wrow)[2],
                                            const Buffer& xb, const uint32_t (&xoff)[NB],
@@ -55,7 +60,9 @@ __device__ __forceinline__ void dot_steps8(uint8_t* stage, const Buffer& wb,
     const bool in = q < n;
     const uint32_t s = in ? (uint32_t)(s0 + step_of(q)) : 0;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) w[u][r] = load16_stream(wb.at(in), woff[r], s * 128);
+    for (int r = 0; r < 4; ++r)
+      w[u][r] = kShared ? load16(wb.at(in), woff[r], s * 128)
+                        : load16_stream(wb.at(in), woff[r], s * 128);
 #pragma unroll
     for (int b = 0; b < NB; ++b) x[u][b] = load16(xb.at(in), xoff[b], s * 128);
   };
@@ -151,7 +158,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_fp8_stream_kernel(
   float* hs = reinterpret_cast<float*>(&stage[0][0]);  // [kRows][kPitch], after the products
   static_assert(kRows * kPitch * 4 <= kWaves * kStageBytes || !kGateUp, "h fits the stage");
 
-  auto pass = [&](auto nb_) __attribute__((always_inline)) {
+  auto pass = [&](auto nb_, auto shared) __attribute__((always_inline)) {
     constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
     uint32_t xoff[NB];
     f32x4 acc[2][NTL];
@@ -174,7 +181,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_fp8_stream_kernel(
         ss[r * kSPitch + k] = r < rows && k < n ? Asc[(int64_t)(row0 + r) * KB + s0 + k] : 0.f;
       }
       __syncthreads();
-      dot_steps8<kGateUp, NB>(stage[wid], wb, woff, wrow, xb, xoff, ss, c0, c1, s0, n,
+      dot_steps8<kGateUp, NB, decltype(shared)::value>(stage[wid], wb, woff, wrow, xb, xoff, ss, c0, c1, s0, n,
                               (tile.ntile + row0) * 5 % n, acc);
     }
     if constexpr (kGateUp) {
@@ -205,9 +212,11 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_fp8_stream_kernel(
         }
     }
   };
-  if (rows <= 8) pass(std::integral_constant<int, 1>{});
-  else if (rows <= 16) pass(std::integral_constant<int, 2>{});
-  else pass(std::integral_constant<int, 4>{});
+  // the expert's other tiles read the same weights
+  if (cnts[e] > kRows) pass(std::integral_constant<int, 4>{}, std::true_type{});
+  else if (rows <= 8) pass(std::integral_constant<int, 1>{}, std::false_type{});
+  else if (rows <= 16) pass(std::integral_constant<int, 2>{}, std::false_type{});
+  else pass(std::integral_constant<int, 4>{}, std::false_type{});
 
   if constexpr (kGateUp) {
     __syncthreads();
