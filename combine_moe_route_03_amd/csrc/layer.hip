@@ -1,7 +1,9 @@
 // layer.hip -- a whole MoE layer for a few tokens (the decode regime: T <= 128
 // tokens and T * k <= 1024 picks): top-k gating (MoE systems survey section
 // 1.1, eq. (2)), the SwiGLU experts (EP flow step 3) and the gate-weighted sum
-// (eq. (1)) in two launches, without a permuted copy of the rows:
+// (eq. (1)) in two launches for up to 8 tokens (one more to route, and one
+// more again where a block cannot route all of them at a time, for more),
+// without a permuted copy of the rows:
 //
 //   gate/up   h[p][j] = bf16( SiLU(x_t . Wg[e][j]) (x_t . Wu[e][j]) ) for every
 //             pick p = t k + i of expert e
@@ -9,13 +11,18 @@
 //
 // Bound by the HBM bytes of the live experts' weights, each read once: a
 // token's rows are small and come from the caches, and the matrix pipes idle
-// mostly. The weights go from memory into registers (nothing re-uses a weight
-// inside a block, so LDS would only add a stop), as the first operand of
-// v_mfma_f32_16x16x32_bf16; the second holds up to 16 tokens of one expert, so
-// an expert with one token costs the same bytes as one with sixteen. 8-bit
-// weights are widened in registers (e4m3 to bf16 is exact) and each 128-column
-// block's product is folded with its scale: half the bytes, the same
-// arithmetic on the tokens.
+// mostly. The weights go from memory into registers past the caches, whole
+// 128-byte lines of 8 rows a load, are turned into fragments in the wave's own
+// LDS, and are the first operand of v_mfma_f32_16x16x32_bf16; the second holds
+// up to 16 tokens of one expert, so an expert with one token costs the same
+// bytes as one with sixteen. A wave takes all tokens of its expert, up to 128,
+// through one pass over its weights. 8-bit weights are widened in registers
+// (e4m3 to bf16 is exact) and each 128-column block's product is folded with
+// its scale: half the bytes, the same arithmetic on the tokens.
+//
+// Measured (H 4096, I 1408, 128 experts, k 8): one token 277 MB in 54 us (gate/up
+// 36, down 18); 128 tokens on 107 experts, most on 8 of them, 3.69 GB in 602 us,
+// 6.1 TB/s (gate/up 398, down 210); on all 128 experts 4.43 GB in 685 us, 6.5 TB/s.
 #include <type_traits>
 
 #include "device.h"
@@ -38,9 +45,11 @@ constexpr int kUpWaves = 4;    // waves of a gate/up block
 constexpr int kUpCols = 8;     // intermediate columns of a unit (8 gate + 8 up rows)
 
 // The live experts in id order and their picks: what both launches need of the
-// routing. A pass over an expert's weights serves kGroup picks, so an expert
-// with more is listed 2 or 4 times (its "parts"), and each list entry ("slot") is
-// one word: expert, first entry in pick, part, picks of the expert (0: no slot).
+// routing. An expert with more than kGroup picks is listed 2 or 4 times (its
+// "parts": its share of the down kernel's work), those experts first: their waves
+// take the longest, and at the list's end the chip idled behind them (128 tokens,
+// most on 8 experts, gate/up: 454 us in id order, 398 so). Each list entry ("slot")
+// is one word: expert, first entry in pick, part, picks of the expert (0: no slot).
 constexpr int kGroup = 32;
 __host__ __device__ __forceinline__ int parts_of(int cnt) { return cnt <= 32 ? 1 : (cnt <= 64 ? 2 : 4); }
 __device__ __forceinline__ uint32_t slot_word(int e, int first, int part, int cnt) {
@@ -76,8 +85,8 @@ struct PlanLds {
 
 // Routes all T tokens (G lanes a token, V >= E / G logits a lane; V = 0: reads
 // the picks of an earlier launch) and groups the picks, all in one block of NT
-// threads. The order of the picks inside a
-// slot is not fixed (LDS atomics), and nothing depends on it: a pick is a
+// threads. The order of the picks inside an
+// expert is not fixed (LDS atomics), and nothing depends on it: a pick is a
 // column of a matrix product and goes to a token of its own. publish: this
 // block also writes the plan, the picks and weights.
 template <int NT, int V, int NP>
@@ -111,13 +120,19 @@ __device__ __forceinline__ void route_and_plan(PlanLds<NP>& P, const float* __re
   __syncthreads();
   for (int p = tid; p < np; p += NT) atomicAdd(&P.cur[P.idx[p]], 1);
   __syncthreads();
-  // exclusive scan over the experts of (slots << 16) + picks
+  // exclusive scan over the experts of three sums in one word: picks, slots of
+  // experts with parts (which are listed first: they take the longest), other slots
+  constexpr int kHot = 11, kCold = 19;
+  static_assert(kMaxPicks < 1 << kHot && 4 * kMaxPicks / 33 < 1 << (kCold - kHot), "fields");
+  const auto word_of = [](int c) {
+    return c == 0 ? 0 : c > kGroup ? (parts_of(c) << kHot) + c : (1 << kCold) + c;
+  };
   const int per = (E + NT - 1) / NT;
   int mine = 0;
   for (int j = 0; j < per; ++j) {
     const int e = tid * per + j;
     const int c = e < E ? P.cur[e] : 0;
-    mine += c > 0 ? (parts_of(c) << 16) + c : 0;
+    mine += word_of(c);
   }
   int incl = mine;
   for (int o = 1; o < kWave; o <<= 1) {
@@ -131,17 +146,19 @@ __device__ __forceinline__ void route_and_plan(PlanLds<NP>& P, const float* __re
     at += w < wid ? P.part[w] : 0;
     total += P.part[w];
   }
+  const auto hot_of = [](int w) { return w >> kHot & ((1 << (kCold - kHot)) - 1); };
+  const int hot = hot_of(total), n = hot + (total >> kCold);
   for (int j = 0; j < per; ++j) {
     const int e = tid * per + j;
     const int c = e < E ? P.cur[e] : 0;
     if (c > 0) {
+      const int first = at & ((1 << kHot) - 1), to = c > kGroup ? hot_of(at) : hot + (at >> kCold);
       const int parts = parts_of(c);
-      for (int q = 0; q < parts; ++q) P.slot[(at >> 16) + q] = slot_word(e, at & 0xFFFF, q, c);
-      P.cur[e] = at & 0xFFFF;
-      at += (parts << 16) + c;
+      for (int q = 0; q < parts; ++q) P.slot[to + q] = slot_word(e, first, q, c);
+      P.cur[e] = first;
+      at += word_of(c);
     }
   }
-  const int n = total >> 16;
   if (tid == 0) P.n = n;
   __syncthreads();
   for (int p = tid; p < np; p += NT) P.pick[atomicAdd(&P.cur[P.idx[p]], 1)] = p;
@@ -171,19 +188,19 @@ struct Step {
   static constexpr int kB = kFp8 ? 2 : 1;  // 128-byte pieces of a token row a step
 };
 
-// Bytes of LDS a wave needs for NB groups of 8 tokens, and the steps in flight
-// that fit 168 registers (three waves a SIMD).
+// Bytes of LDS a wave needs for NB groups of 8 tokens, and the steps in flight: what
+// fits 168 registers (three waves a SIMD), or 128 with 8 rows (four).
 constexpr int stage_bytes(int NB) { return 2048 + NB * 1024; }
 template <bool kFp8, int RW, int NB>
 constexpr int kRing = kFp8 ? (NB == 1 ? (RW == 8 ? 6 : 4) : (NB == 2 ? 3 : 2))
-                           : (NB == 1 ? (RW == 8 ? 8 : 6) : (NB == 2 ? 4 : 3));
+                           : (NB == 1 ? (RW == 8 ? 8 : 6) : (NB == 2 ? 4 : (RW == 8 ? 2 : 3)));
 
 // acc[t] += the products of the unit's rows with NB x 8 tokens over n K steps
-// from s0, beginning with step s0 + rot. woff: byte offsets in wb of the lane's two rows at
-// its chunk (RW = 8: the first only), wrow their LDS rows; xoff[b]: in xb of
-// its token of group b at its chunk (kOutside without a token); c0, c1 (e4m3): scales of D registers 0-1 and 2-3, one
-// a step (uniform: scalar loads; through the vector path they were two of six
-// load instructions a step).
+// from s0, beginning with step s0 + rot. woff: byte offsets in wb of the lane's two
+// rows at its chunk (RW = 8: the first only), wrow their LDS rows; xoff[b]: in xb
+// of its token of group b at its chunk (kOutside without a token); c0, c1 (e4m3):
+// scales of D registers 0-1 and 2-3, one a step (uniform: scalar loads; through the
+// vector path they were two of six load instructions a step).
 template <bool kFp8, int RW, int NB, int D>
 __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
                                           const uint32_t (&woff)[2], const int (&wrow)[2],
@@ -274,15 +291,114 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
   }
 }
 
+// The same for NG groups of kGroup tokens, each step's weights loaded once for all of
+// them: xoff[q], acc[q] are group q's; XD: groups of tokens in flight. (A pass over
+// the weights for each group, 128 tokens, most on 8 experts: gate/up 478 against
+// 454 us, down 249 against 212; memory reads 2.84 and 1.51 GB for 2.47 and 1.23 GB.)
+template <bool kFp8, int RW, int NG, int XD>
+__device__ __forceinline__ void dot_steps_groups(uint8_t* stage, const Buffer& wb,
+                                                 const uint32_t (&woff)[2], const int (&wrow)[2],
+                                                 const Buffer& xb, const uint32_t (&xoff)[NG][4],
+                                                 const float* __restrict__ c0,
+                                                 const float* __restrict__ c1, int s0, int n,
+                                                 int rot, f32x4 (&acc)[NG][2]) {
+  constexpr int kB = Step<kFp8>::kB, RI = RW / 8, kM = kFp8 ? 2 : 1;
+  static_assert(2 * NG % XD == 0, "two steps' groups are whole turns of the ring");
+  const int lane = threadIdx.x & (kWave - 1);
+  const int lr = lane >> 3, lc = lane & 7, i = lane & 15, g = lane >> 4;
+  v4u w[2][RI], x[XD][4][kB];
+  float a0[2], a1[2];
+  const auto step_at = [&](int q) -> uint32_t {
+    const int o = q + rot;
+    return q < n ? (uint32_t)(s0 + (o >= n ? o - n : o)) : 0;
+  };
+  auto load_w = [&](int u, int q) __attribute__((always_inline)) {
+    const uint32_t s = step_at(q);
+#pragma unroll
+    for (int r = 0; r < RI; ++r) w[u][r] = load16_stream(wb.at(q < n), woff[r], s * 128);
+    if constexpr (kFp8) {
+      a0[u] = c0[q < n ? s : (uint32_t)s0];
+      a1[u] = c1[q < n ? s : (uint32_t)s0];
+    }
+  };
+  auto load_x = [&](int u, int q, int grp) __attribute__((always_inline)) {
+    const uint32_t s = step_at(q);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int p = 0; p < kB; ++p)
+        x[u][b][p] = load16(xb.at(q < n), xoff[grp][b], s * (Step<kFp8>::kCols * 2) + 128 * p);
+  };
+  uint8_t* xs = stage + 2048;
+  const int arow = RW == 8 ? i & 7 : i;
+  load_w(0, 0);
+  load_w(1, 1);
+#pragma unroll
+  for (int e = 0; e < XD; ++e) load_x(e, e / NG, e % NG);
+  for (int q = 0; q < n; q += 2) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int r = 0; r < RI; ++r) *reinterpret_cast<v4u*>(stage + tile_at(wrow[r], lc)) = w[u][r];
+      __builtin_amdgcn_wave_barrier();
+      bf16x8 a[2][kM];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if constexpr (kFp8) {
+          const v4u v = *reinterpret_cast<const v4u*>(stage + tile_at(arow, 4 * m + g));
+          a[m][0] = widen8(v[0], v[1]);
+          a[m][1] = widen8(v[2], v[3]);
+        } else {
+          a[m][0] = *reinterpret_cast<const bf16x8*>(stage + tile_at(arow, 4 * m + g));
+        }
+      }
+      const float f0 = kFp8 ? a0[u] : 0.f, f1 = kFp8 ? a1[u] : 0.f;
+      load_w(u, q + u + 2);
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) {
+        const int v = (u * NG + grp) % XD;
+        f32x4 d[2] = {acc[grp][0], acc[grp][1]};
+        if constexpr (kFp8) d[0] = d[1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < kB; ++p) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            *reinterpret_cast<v4u*>(xs + tile_at(8 * b + lr, lc)) = x[v][b][p];
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  kFp8 ? a[p][m] : a[m][0],
+                  *reinterpret_cast<const bf16x8*>(
+                      xs + tile_at(16 * t + i, kFp8 ? 2 * g + m : 4 * m + g)),
+                  d[t], 0, 0, 0);
+          __builtin_amdgcn_wave_barrier();
+        }
+        load_x(v, q + u + (grp + XD) / NG, (grp + XD) % NG);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if constexpr (kFp8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[grp][t][r] = __builtin_fmaf(d[t][r], r < 2 ? f0 : f1, acc[grp][t][r]);
+          } else {
+            acc[grp][t] = d[t];
+          }
+      }
+    }
+  }
+}
+
 // Gate/up: a unit is kUpCols intermediate columns of one live expert (8 gate and
-// 8 up rows) for kGroup of its picks, computed by KS waves, each a part of the K
+// 8 up rows) for all its picks, computed by KS waves, each a part of the K
 // steps (their sums are added in LDS in a fixed order); a block has kUpWaves /
-// KS units, or, of an expert with more picks, the same columns' units for all
-// its groups (the waves then read the same weights at one time). MFMA row i is gate row 2 (i / 4) + i % 4 for i % 4 < 2, else the up
+// KS units. MFMA row i is gate row 2 (i / 4) + i % 4 for i % 4 < 2, else the up
 // row of the same column, so a lane's four results are g, g, u, u of two
 // neighbouring columns. kV > 0: the block routes all tokens itself (kV logits a
 // lane), block (0, 0) publishes; kV = 0: the plan is in the workspace. kMaxNB:
-// most eights of picks a unit can have.
+// most eights of picks in a pass (1 with up to kRouteT tokens).
 template <int kV, int KS, bool kFp8, int kMaxNB>
 __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void layer_gate_up_kernel(
     const float* __restrict__ logits, const uint16_t* __restrict__ x, int T, int H, int E, int k,
@@ -309,17 +425,10 @@ __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void 
   }
   word = __builtin_amdgcn_readfirstlane(word);
   const int e = slot_expert(word);
-  int cnt = slot_count(word);
-  if (cnt == 0) return;  // uniform over the block
-  const int ks = wid % KS;
-  // with parts (KS = 1 then): wave w takes group w % parts, the slot a share of the columns
-  const int parts = KS == 1 ? parts_of(cnt) : 1, grp = KS == 1 ? wid % parts : 0;
-  const int unit = KS == 1 ? (slot_part(word) * (int)gridDim.x + (int)blockIdx.x) * (kUpWaves / parts) +
-                                 wid / parts
-                           : (int)blockIdx.x * (kUpWaves / KS) + wid / KS;
-  pick += slot_first(word) + grp * kGroup;
-  cnt -= grp * kGroup;
-  if (KS == 1 && cnt <= 0) return;  // three groups of four
+  const int cnt = slot_count(word);
+  if (cnt == 0 || slot_part(word) > 0) return;  // uniform over the block
+  const int ks = wid % KS, unit = (int)blockIdx.x * (kUpWaves / KS) + wid / KS;
+  pick += slot_first(word);
   const int j0 = unit * kUpCols;
   const int i = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
   constexpr int kWB = kFp8 ? 1 : 2;  // bytes of a weight
@@ -336,15 +445,21 @@ __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void 
     c0 = wsc + ((int64_t)e * (2 * I / kQuantBlock) + j0 / kQuantBlock) * steps;
     c1 = c0 + (int64_t)(I / kQuantBlock) * steps;
   }
+  const auto offset_of = [&](int c) {
+    return c < cnt ? (uint32_t)(pick[c] / k) * (uint32_t)(2 * H) + 16 * lc : kOutside;
+  };
+  const auto store = [&](int c, const f32x4& v, bool on) __attribute__((always_inline)) {
+    if (c < cnt && on) {
+      const uint32_t hv = bf16x2_rne(silu(v[0]) * v[2], silu(v[1]) * v[3]);
+      *reinterpret_cast<uint32_t*>(h + (int64_t)pick[c] * I + j0 + 2 * g) = hv;
+    }
+  };
   auto pass = [&](auto nb_) __attribute__((always_inline)) {
     constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
     uint32_t xoff[NB];
     f32x4 acc[NTL];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int c = 8 * b + lr;
-      xoff[b] = c < cnt ? (uint32_t)(pick[c] / k) * (uint32_t)(2 * H) + 16 * lc : kOutside;
-    }
+    for (int b = 0; b < NB; ++b) xoff[b] = offset_of(8 * b + lr);
 #pragma unroll
     for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
     dot_steps<kFp8, 16, NB, kRing<kFp8, 16, NB>>(stage[wid], wb, woff, wrow, xb, xoff, c0, c1, s0,
@@ -363,18 +478,34 @@ __global__ __launch_bounds__(kWave * kUpWaves, kFp8 || kMaxNB > 1 ? 3 : 4) void 
 #pragma unroll
         for (int q = 1; q < KS; ++q) v += red[wid - ks + q][t][lane];
       }
-      const int c = 16 * t + i;
-      if (c < cnt && (NB > 1 || i < 8)) {
-        const uint32_t hv = bf16x2_rne(silu(v[0]) * v[2], silu(v[1]) * v[3]);
-        *reinterpret_cast<uint32_t*>(h + (int64_t)pick[c] * I + j0 + 2 * g) = hv;
-      }
+      store(16 * t + i, v, NB > 1 || i < 8);
     }
+  };
+  auto groups = [&](auto ng_) __attribute__((always_inline)) {
+    constexpr int NG = decltype(ng_)::value;
+    uint32_t xoff[NG][4];
+    f32x4 acc[NG][2];
+#pragma unroll
+    for (int q = 0; q < NG; ++q)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) xoff[q][b] = offset_of(q * kGroup + 8 * b + lr);
+#pragma unroll
+    for (int q = 0; q < NG; ++q) acc[q][0] = acc[q][1] = f32x4{0, 0, 0, 0};
+    dot_steps_groups<kFp8, 16, NG, kFp8 ? 1 : 2>(stage[wid], wb, woff, wrow, xb, xoff, c0, c1, s0,
+                                                 n, rot, acc);
+#pragma unroll
+    for (int q = 0; q < NG; ++q)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) store(q * kGroup + 16 * t + i, acc[q][t], true);
   };
   if (kMaxNB == 1 || cnt <= 8) {
     pass(std::integral_constant<int, 1>{});
   } else if constexpr (kMaxNB > 1) {
+    static_assert(KS == 1, "the groups' sums are not joined");
     if (cnt <= 16) pass(std::integral_constant<int, 2>{});
-    else pass(std::integral_constant<int, 4>{});
+    else if (cnt <= kGroup) pass(std::integral_constant<int, 4>{});
+    else if (cnt <= 2 * kGroup) groups(std::integral_constant<int, 2>{});
+    else groups(std::integral_constant<int, 4>{});
   }
 }
 
@@ -390,10 +521,12 @@ __global__ __launch_bounds__(1024) void layer_plan_kernel(const float* __restric
 }
 
 // Down and combine: a block computes RW columns of y for all tokens. The K steps
-// of all slots in a row are cut into one range a wave; at the end of an
-// expert's part of its range a wave adds gate weight x result to its own fp32
+// of all slots in a row are cut into one range a wave (an expert's parts are one
+// run of them, in which a step of its weights counts once a part); at the end of
+// an expert's share of its range a wave adds gate weight x result to its own fp32
 // rows of y in LDS (an expert's picks are different tokens), and the waves' rows
-// are added in a fixed order at the end.
+// are added in a fixed order at the end. Sixteen waves have registers for two
+// groups of tokens at a time, so four take two passes.
 template <bool kFp8, int RW, int kMaxNB, int DW>
 __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
     const uint16_t* __restrict__ h, int T, int H, int k, int I, int slots,
@@ -431,51 +564,74 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
   const int wrow[2] = {lr, 8 + lr};
   while (at < end) {
     const int slot = at / steps;
-    const int s0 = at - slot * steps;
-    const int s1 = end - at < steps - s0 ? s0 + (end - at) : steps;
-    at += s1 - s0;
-    const int rot = blockIdx.x * 5 % (s1 - s0);
     const uint32_t word = __builtin_amdgcn_readfirstlane(sl[slot]);
-    const int e = slot_expert(word), grp = slot_part(word);
-    const int cnt = slot_count(word) - grp * kGroup;  // this part's picks (and further ones)
-    if (cnt <= 0) continue;                           // three groups of four
-    const uint16_t* pick = pk + slot_first(word) + grp * kGroup;
+    const int e = slot_expert(word), cnt = slot_count(word), parts = parts_of(cnt);
+    // the parts of an expert are one run of parts * steps entries, parts of them a step
+    const int from = at - (slot - slot_part(word)) * steps;
+    const int to = end - at < parts * steps - from ? from + (end - at) : parts * steps;
+    at += to - from;
+    const int s0 = (from + parts - 1) / parts, s1 = (to + parts - 1) / parts;
+    if (s0 == s1) continue;
+    const int rot = blockIdx.x * 5 % (s1 - s0);
+    const uint16_t* pick = pk + slot_first(word);
     const Buffer wb = {w + (int64_t)e * H * I * kWB, (uint32_t)H * (uint32_t)(I * kWB)};
     const float* sc = nullptr;
     if constexpr (kFp8)
       sc = wsc + ((int64_t)e * (H / kQuantBlock) + c0 / kQuantBlock) * steps;
+    // gate weight x result of the 16 picks from c0, to the wave's own rows of y
+    auto add = [&](int c0, const f32x4& d, bool on) __attribute__((always_inline)) {
+      const int c = c0 + i;
+      if (c < cnt && on && (RW == 16 || g < 2)) {
+        const int p = pick[c];
+        const float gp = gw[p];
+        f32x4* dst = reinterpret_cast<f32x4*>(mine + (p / k) * RW + 4 * g);
+        f32x4 v = *dst;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gp, d[r], v[r]);
+        *dst = v;
+      }
+    };
+    const auto offset_of = [&](int c) {
+      return c < cnt ? (uint32_t)pick[c] * (uint32_t)(2 * I) + 16 * lc : kOutside;
+    };
     auto pass = [&](auto nb_) __attribute__((always_inline)) {
       constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
       uint32_t hoff[NB];
       f32x4 acc[NTL];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int c = 8 * b + lr;
-        hoff[b] = c < cnt ? (uint32_t)pick[c] * (uint32_t)(2 * I) + 16 * lc : kOutside;
-      }
+      for (int b = 0; b < NB; ++b) hoff[b] = offset_of(8 * b + lr);
 #pragma unroll
       for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
       dot_steps<kFp8, RW, NB, kRing<kFp8, RW, NB>>(stage + wid * stage_bytes(kMaxNB), wb, woff, wrow,
                                                 hb, hoff, sc, sc, s0, s1 - s0, rot, acc);
 #pragma unroll
-      for (int t = 0; t < NTL; ++t) {
-        const int c = 16 * t + i;
-        if (c < cnt && (NB > 1 || i < 8) && (RW == 16 || g < 2)) {
-          const int p = pick[c];
-          const float gp = gw[p];
-          f32x4* dst = reinterpret_cast<f32x4*>(mine + (p / k) * RW + 4 * g);
-          f32x4 v = *dst;
+      for (int t = 0; t < NTL; ++t) add(16 * t, acc[t], NB > 1 || i < 8);
+    };
+    auto groups = [&](auto ng_, int first) __attribute__((always_inline)) {
+      constexpr int NG = decltype(ng_)::value;
+      uint32_t hoff[NG][4];
+      f32x4 acc[NG][2];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gp, acc[t][r], v[r]);
-          *dst = v;
-        }
-      }
+      for (int q = 0; q < NG; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) hoff[q][b] = offset_of(first + q * kGroup + 8 * b + lr);
+#pragma unroll
+      for (int q = 0; q < NG; ++q) acc[q][0] = acc[q][1] = f32x4{0, 0, 0, 0};
+      dot_steps_groups<kFp8, RW, NG, (DW == 16 ? (kFp8 ? 2 : 1) : 4) / (kFp8 ? 2 : 1)>(
+          stage + wid * stage_bytes(kMaxNB), wb, woff, wrow, hb, hoff, sc, sc, s0, s1 - s0, rot, acc);
+#pragma unroll
+      for (int q = 0; q < NG; ++q)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) add(first + q * kGroup + 16 * t, acc[q][t], true);
     };
     if (kMaxNB == 1 || cnt <= 8) {
       pass(std::integral_constant<int, 1>{});
     } else if constexpr (kMaxNB > 1) {
       if (cnt <= 16) pass(std::integral_constant<int, 2>{});
-      else pass(std::integral_constant<int, 4>{});
+      else if (cnt <= kGroup) pass(std::integral_constant<int, 4>{});
+      else if (DW == 8 && parts == 4) groups(std::integral_constant<int, DW == 8 ? 4 : 2>{}, 0);
+      else
+        for (int q = 0; q < parts; q += 2) groups(std::integral_constant<int, 2>{}, q * kGroup);
     }
   }
   __syncthreads();
@@ -568,7 +724,8 @@ hipError_t run_layer(const float* logits, const void* x, int T, int H, int E, in
     using I8 = std::integral_constant<int, 8>;
     using I16 = std::integral_constant<int, 16>;
     if (T <= 8) return down(rw, I1{}, I16{});
-    if (decltype(rw)::value == 8 && lds(8, 4, 16) <= kLdsBytes) return down(rw, I4{}, I16{});
+    if constexpr (decltype(rw)::value == 8)
+      if (lds(8, 4, 16) <= kLdsBytes) return down(rw, I4{}, I16{});
     return down(rw, I4{}, I8{});
   };
   // 16 columns a block where that makes a block for every compute unit

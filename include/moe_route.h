@@ -401,8 +401,8 @@ size_t moe_layer_workspace_bytes(const moe_shape* shape, int32_t I);
  * all sums in fp32 (finite operands as in moe_expert_swiglu). Differs from
  * moe_route + moe_dispatch + moe_expert_swiglu + moe_combine in that the
  * experts' outputs are not rounded to bf16 before they are weighted. Only live
- * experts' weights are read, once (w_down again for every further 32 picks of an
- * expert). Two launches for T <= 8, else one more to route and one more again
+ * experts' weights are read, once (w_down twice for an expert with more than 64
+ * picks, where H < 4096). Two launches for T <= 8, else one more to route and one more again
  * where a block cannot route all tokens at a time.
  * weight_dtype MOE_BF16: w_gate_up [E][2I][H], w_down [E][H][I] bf16, the scales
  * unused (NULL). MOE_F8E4M3: the same in e4m3 with s_gate_up [E][2I/128][H/128],

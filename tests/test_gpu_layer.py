@@ -66,6 +66,19 @@ def test_layer(T, H, E, k, I, routing, fp8):
     assert float(err.max()) <= 0, f"{float(err.max())} over the bound"
 
 
+# Experts with more picks than one group of 32, through every shape of the down kernel: 8 or
+# 16 columns a block, 8 or 16 waves; two, three and four groups.
+GROUPS = [(50, 128, 5, 2, 256, "one"), (100, 128, 3, 2, 128, "one"), (96, 256, 70, 4, 128, "hot"),
+          (128, 256, 5, 3, 384, "hot"), (40, 4096, 2, 1, 128, "one"), (70, 4096, 1, 1, 128, "iid"),
+          (128, 4096, 3, 2, 256, "one"), (128, 4096, 40, 2, 128, "hot")]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,E,k,I,routing", GROUPS)
+def test_layer_many_picks_an_expert(T, H, E, k, I, routing, fp8):
+    test_layer(T, H, E, k, I, routing, fp8)
+
+
 def test_layer_agrees_with_the_separate_steps():
     """moe_route, moe_dispatch, moe_expert_swiglu and moe_combine on the same
     inputs: the same picks and weights bit for bit; y differs by the rounding of
