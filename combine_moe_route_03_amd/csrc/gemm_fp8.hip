@@ -503,10 +503,12 @@ hipError_t run_gemm(const void* a, const float* asc, int64_t rows, int E, const 
 
 // Rows an expert on average up to which the streamed products (tiles of 32 rows)
 // are the faster. 128 experts, N 2816, K 4096, even routing: 16 rows 258 against
-// 323 us, 24 rows 291 against 327, 32 rows (half the experts take two tiles) 416
-// against 332; K 1408, N 4096: 16 rows 140 against 171, 32 rows 228 against 182.
+// 318 us, 24 rows 283 against 321, 28 rows 316 against 326, 32 rows (half the
+// experts take two tiles) 343 against 328; N 4096, K 1408: 16 rows 140 against
+// 159, 28 rows 163 against 166, 32 rows 181 against 168. Most picks on 8 experts,
+// N 2816: 8 rows 198 against 264, 24 rows 287 against 346.
 // One K step is too short for the tiled kernel's stream of loads.
-constexpr int kFewRows = 24;
+constexpr int kFewRows = 28;
 bool few_rows(int64_t rows, int E, int K) { return K == kBK || rows <= (int64_t)kFewRows * E; }
 
 }  // namespace

@@ -21,8 +21,8 @@
 // its scale: half the bytes, the same arithmetic on the tokens.
 //
 // Measured (H 4096, I 1408, 128 experts, k 8): one token 277 MB in 54 us (gate/up
-// 36, down 18); 128 tokens on 107 experts, most on 8 of them, 3.69 GB in 602 us,
-// 6.1 TB/s (gate/up 398, down 210); on all 128 experts 4.43 GB in 685 us, 6.5 TB/s.
+// 36, down 18); 128 tokens on 107 experts, most on 8 of them, 3.69 GB in 600 us,
+// 6.1 TB/s (gate/up 396, down 201); on all 128 experts 4.43 GB in 683 us, 6.5 TB/s.
 #include <type_traits>
 
 #include "device.h"
@@ -195,6 +195,65 @@ template <bool kFp8, int RW, int NB>
 constexpr int kRing = kFp8 ? (NB == 1 ? (RW == 8 ? 6 : 4) : (NB == 2 ? 3 : 2))
                            : (NB == 1 ? (RW == 8 ? 8 : 6) : (NB == 2 ? 4 : (RW == 8 ? 2 : 3)));
 
+// acc[t] += the product of one K step: w, the lane's 16 bytes of two rows (RW = 8: of
+// one) and x, of its token of each group of 8; wrow: LDS rows of the weight rows;
+// f0, f1 (e4m3): scales of D registers 0-1 and 2-3.
+template <bool kFp8, int RW, int NB>
+__device__ __forceinline__ void step_product(uint8_t* stage, const int (&wrow)[2],
+                                             const v4u (&w)[RW / 8],
+                                             const v4u (&x)[NB][Step<kFp8>::kB], float f0, float f1,
+                                             f32x4 (&acc)[(NB + 1) / 2]) {
+  constexpr int NTL = (NB + 1) / 2;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int lr = lane >> 3, lc = lane & 7, i = lane & 15, g = lane >> 4;
+  uint8_t* xs = stage + 2048;
+  const int arow = RW == 8 ? i & 7 : i;  // rows 8-15 of an 8-row unit repeat: not used
+#pragma unroll
+  for (int r = 0; r < RW / 8; ++r) *reinterpret_cast<v4u*>(stage + tile_at(wrow[r], lc)) = w[r];
+  auto put_x = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) *reinterpret_cast<v4u*>(xs + tile_at(8 * b + lr, lc)) = x[b][p];
+    __builtin_amdgcn_wave_barrier();
+  };
+  put_x(0);
+  // a token tile's rows; with one group of 8 its rows twice (columns 8-15 unused)
+  auto trow = [&](int t) { return NB == 1 ? i & 7 : 16 * t + i; };
+  if constexpr (kFp8) {
+    f32x4 d[NTL];
+#pragma unroll
+    for (int t = 0; t < NTL; ++t) d[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (m > 0) put_x(m);
+      const v4u q = *reinterpret_cast<const v4u*>(stage + tile_at(arow, 4 * m + g));
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const bf16x8 a = widen8(q[2 * hh], q[2 * hh + 1]);
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+          d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a, *reinterpret_cast<const bf16x8*>(xs + tile_at(trow(t), 2 * g + hh)), d[t], 0, 0, 0);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int t = 0; t < NTL; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[t][r] = __builtin_fmaf(d[t][r], r < 2 ? f0 : f1, acc[t][r]);
+  } else {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const bf16x8 a = *reinterpret_cast<const bf16x8*>(stage + tile_at(arow, 4 * m + g));
+#pragma unroll
+      for (int t = 0; t < NTL; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            a, *reinterpret_cast<const bf16x8*>(xs + tile_at(trow(t), 4 * m + g)), acc[t], 0, 0, 0);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
 // acc[t] += the products of the unit's rows with NB x 8 tokens over n K steps
 // from s0, beginning with step s0 + rot. woff: byte offsets in wb of the lane's two
 // rows at its chunk (RW = 8: the first only), wrow their LDS rows; xoff[b]: in xb
@@ -208,9 +267,7 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
                                           const float* __restrict__ c0,
                                           const float* __restrict__ c1,
                                           int s0, int n, int rot, f32x4 (&acc)[(NB + 1) / 2]) {
-  constexpr int kB = Step<kFp8>::kB, NTL = (NB + 1) / 2, RI = RW / 8;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int lr = lane >> 3, lc = lane & 7, i = lane & 15, g = lane >> 4;
+  constexpr int kB = Step<kFp8>::kB, RI = RW / 8;
   v4u w[D][RI], x[D][NB][kB];
   float a0[D], a1[D];
   auto load = [&](int u, int q) __attribute__((always_inline)) {
@@ -230,62 +287,12 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
       a1[u] = c1[in ? s : (uint32_t)s0];
     }
   };
-  uint8_t* xs = stage + 2048;
-  const int arow = RW == 8 ? i & 7 : i;  // rows 8-15 of an 8-row unit repeat: not used
-  auto compute = [&](int u) __attribute__((always_inline)) {
-#pragma unroll
-    for (int r = 0; r < RI; ++r) *reinterpret_cast<v4u*>(stage + tile_at(wrow[r], lc)) = w[u][r];
-    auto put_x = [&](int p) __attribute__((always_inline)) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        *reinterpret_cast<v4u*>(xs + tile_at(8 * b + lr, lc)) = x[u][b][p];
-      __builtin_amdgcn_wave_barrier();
-    };
-    put_x(0);
-    // a token tile's rows; with one group of 8 its rows twice (columns 8-15 unused)
-    auto trow = [&](int t) { return NB == 1 ? i & 7 : 16 * t + i; };
-    if constexpr (kFp8) {
-      f32x4 d[NTL];
-#pragma unroll
-      for (int t = 0; t < NTL; ++t) d[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (m > 0) put_x(m);
-        const v4u q = *reinterpret_cast<const v4u*>(stage + tile_at(arow, 4 * m + g));
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const bf16x8 a = widen8(q[2 * hh], q[2 * hh + 1]);
-#pragma unroll
-          for (int t = 0; t < NTL; ++t)
-            d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                a, *reinterpret_cast<const bf16x8*>(xs + tile_at(trow(t), 2 * g + hh)),
-                d[t], 0, 0, 0);
-        }
-        __builtin_amdgcn_wave_barrier();
-      }
-#pragma unroll
-      for (int t = 0; t < NTL; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[t][r] = __builtin_fmaf(d[t][r], r < 2 ? a0[u] : a1[u], acc[t][r]);
-    } else {
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8*>(stage + tile_at(arow, 4 * m + g));
-#pragma unroll
-        for (int t = 0; t < NTL; ++t)
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              a, *reinterpret_cast<const bf16x8*>(xs + tile_at(trow(t), 4 * m + g)), acc[t], 0, 0, 0);
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
-  };
 #pragma unroll
   for (int u = 0; u < D; ++u) load(u, u);
   for (int q = 0; q < n; q += D) {
 #pragma unroll
     for (int u = 0; u < D; ++u) {
-      compute(u);
+      step_product<kFp8, RW, NB>(stage, wrow, w[u], x[u], kFp8 ? a0[u] : 0.f, kFp8 ? a1[u] : 0.f, acc);
       load(u, q + u + D);
     }
   }
@@ -562,10 +569,104 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
   const uint32_t woff[2] = {(uint32_t)(c0 + lr) * (uint32_t)(I * kWB) + 16 * lc,
                             (uint32_t)(c0 + 8 + lr) * (uint32_t)(I * kWB) + 16 * lc};
   const int wrow[2] = {lr, 8 + lr};
+  uint8_t* const my_stage = stage + wid * stage_bytes(kMaxNB);
+  const auto weights_of = [&](uint32_t word) -> Buffer {
+    return {w + (int64_t)slot_expert(word) * H * I * kWB, (uint32_t)H * (uint32_t)(I * kWB)};
+  };
+  const auto scales_of = [&](uint32_t word) -> const float* {
+    return kFp8 ? wsc + ((int64_t)slot_expert(word) * (H / kQuantBlock) + c0 / kQuantBlock) * steps
+                : nullptr;
+  };
+  const auto offset_of = [&](uint32_t word, int c) {
+    return c < slot_count(word)
+               ? (uint32_t)pk[slot_first(word) + c] * (uint32_t)(2 * I) + 16 * lc
+               : kOutside;
+  };
+  // gate weight x result of the 16 picks from p0, to the wave's own rows of y
+  auto add = [&](uint32_t word, int p0, const f32x4& d, bool on) __attribute__((always_inline)) {
+    const int c = p0 + i;
+    if (c < slot_count(word) && on && (RW == 16 || g < 2)) {
+      const int p = pk[slot_first(word) + c];
+      const float gp = gw[p];
+      f32x4* dst = reinterpret_cast<f32x4*>(mine + (p / k) * RW + 4 * g);
+      f32x4 v = *dst;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gp, d[r], v[r]);
+      *dst = v;
+    }
+  };
+  // The run of experts of up to 8 picks (the most of them) that begins here: their
+  // K steps are one stream, the loads run into the next expert while this one's last
+  // steps are computed (each expert a stream of its own: 17 tokens, H 2048, 64 experts
+  // of 8 bits 43 against 34 us; 128 tokens, H 4096, 128 experts 211 against 201).
+  auto run_of_few = [&]() __attribute__((always_inline)) {
+    constexpr int D = kRing<kFp8, RW, 1>, kB = Step<kFp8>::kB, RI = RW / 8;
+    v4u wv[D][RI], x[D][1][kB];
+    float a0[D];
+    // loads: the slot they are in, its steps [s0, s0 + n) beginning with s0 + o, left of them
+    int lslot = at / steps, s0 = at - lslot * steps, next = s0, n = 0, o = 0, left = 0, total = 0;
+    bool on = true;
+    Buffer wb = {w, 0};
+    uint32_t hoff = kOutside;
+    const float* sc = wsc;
+    auto enter = [&]() __attribute__((always_inline)) {
+      const uint32_t word =
+          at + total < end ? (uint32_t)__builtin_amdgcn_readfirstlane(sl[lslot]) : 0;
+      on = slot_count(word) > 0 && slot_count(word) <= 8;
+      if (on) {
+        s0 = next;
+        n = steps - s0 < end - at - total ? steps - s0 : end - at - total;
+        wb = weights_of(word);
+        sc = scales_of(word);
+        hoff = offset_of(word, lr);
+        o = blockIdx.x * 5 % n;
+        left = n;
+        total += n;
+        next = 0;
+        ++lslot;
+      }
+    };
+    auto load = [&](int u) __attribute__((always_inline)) {
+      const uint32_t s = on ? (uint32_t)(s0 + o) : 0;
+#pragma unroll
+      for (int r = 0; r < RI; ++r) wv[u][r] = load16_stream(wb.at(on), woff[r], s * 128);
+#pragma unroll
+      for (int p = 0; p < kB; ++p)
+        x[u][0][p] = load16(hb.at(on), hoff, s * (Step<kFp8>::kCols * 2) + 128 * p);
+      if constexpr (kFp8) a0[u] = sc[on ? s : (uint32_t)s0];
+      o = o + 1 == n ? 0 : o + 1;
+      if (on && --left == 0) enter();
+    };
+    enter();
+    int cslot = at / steps, cleft = n, done = 0;  // the slot computed, what is left of it
+    f32x4 acc[1] = {f32x4{0, 0, 0, 0}};
+#pragma unroll
+    for (int u = 0; u < D; ++u) load(u);
+    for (int q = 0; q < total; q += D) {
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        step_product<kFp8, RW, 1>(my_stage, wrow, wv[u], x[u], kFp8 ? a0[u] : 0.f,
+                                  kFp8 ? a0[u] : 0.f, acc);
+        ++done;
+        if (--cleft == 0) {
+          add(__builtin_amdgcn_readfirstlane(sl[cslot++]), 0, acc[0], i < 8);
+          acc[0] = f32x4{0, 0, 0, 0};
+          // the loads are in the next slot of the run already, if there is one
+          cleft = total - done < steps ? total - done : steps;
+        }
+        load(u);
+      }
+    }
+    at += total;
+  };
   while (at < end) {
     const int slot = at / steps;
     const uint32_t word = __builtin_amdgcn_readfirstlane(sl[slot]);
-    const int e = slot_expert(word), cnt = slot_count(word), parts = parts_of(cnt);
+    const int cnt = slot_count(word), parts = parts_of(cnt);
+    if (kMaxNB == 1 || cnt <= 8) {
+      run_of_few();
+      continue;
+    }
     // the parts of an expert are one run of parts * steps entries, parts of them a step
     const int from = at - (slot - slot_part(word)) * steps;
     const int to = end - at < parts * steps - from ? from + (end - at) : parts * steps;
@@ -573,39 +674,20 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
     const int s0 = (from + parts - 1) / parts, s1 = (to + parts - 1) / parts;
     if (s0 == s1) continue;
     const int rot = blockIdx.x * 5 % (s1 - s0);
-    const uint16_t* pick = pk + slot_first(word);
-    const Buffer wb = {w + (int64_t)e * H * I * kWB, (uint32_t)H * (uint32_t)(I * kWB)};
-    const float* sc = nullptr;
-    if constexpr (kFp8)
-      sc = wsc + ((int64_t)e * (H / kQuantBlock) + c0 / kQuantBlock) * steps;
-    // gate weight x result of the 16 picks from c0, to the wave's own rows of y
-    auto add = [&](int c0, const f32x4& d, bool on) __attribute__((always_inline)) {
-      const int c = c0 + i;
-      if (c < cnt && on && (RW == 16 || g < 2)) {
-        const int p = pick[c];
-        const float gp = gw[p];
-        f32x4* dst = reinterpret_cast<f32x4*>(mine + (p / k) * RW + 4 * g);
-        f32x4 v = *dst;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(gp, d[r], v[r]);
-        *dst = v;
-      }
-    };
-    const auto offset_of = [&](int c) {
-      return c < cnt ? (uint32_t)pick[c] * (uint32_t)(2 * I) + 16 * lc : kOutside;
-    };
+    const Buffer wb = weights_of(word);
+    const float* sc = scales_of(word);
     auto pass = [&](auto nb_) __attribute__((always_inline)) {
       constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
       uint32_t hoff[NB];
       f32x4 acc[NTL];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) hoff[b] = offset_of(8 * b + lr);
+      for (int b = 0; b < NB; ++b) hoff[b] = offset_of(word, 8 * b + lr);
 #pragma unroll
       for (int t = 0; t < NTL; ++t) acc[t] = f32x4{0, 0, 0, 0};
-      dot_steps<kFp8, RW, NB, kRing<kFp8, RW, NB>>(stage + wid * stage_bytes(kMaxNB), wb, woff, wrow,
-                                                hb, hoff, sc, sc, s0, s1 - s0, rot, acc);
+      dot_steps<kFp8, RW, NB, kRing<kFp8, RW, NB>>(my_stage, wb, woff, wrow, hb, hoff, sc, sc, s0,
+                                                   s1 - s0, rot, acc);
 #pragma unroll
-      for (int t = 0; t < NTL; ++t) add(16 * t, acc[t], NB > 1 || i < 8);
+      for (int t = 0; t < NTL; ++t) add(word, 16 * t, acc[t], true);
     };
     auto groups = [&](auto ng_, int first) __attribute__((always_inline)) {
       constexpr int NG = decltype(ng_)::value;
@@ -614,19 +696,17 @@ __global__ __launch_bounds__(kWave * DW) void layer_down_kernel(
 #pragma unroll
       for (int q = 0; q < NG; ++q)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) hoff[q][b] = offset_of(first + q * kGroup + 8 * b + lr);
+        for (int b = 0; b < 4; ++b) hoff[q][b] = offset_of(word, first + q * kGroup + 8 * b + lr);
 #pragma unroll
       for (int q = 0; q < NG; ++q) acc[q][0] = acc[q][1] = f32x4{0, 0, 0, 0};
-      dot_steps_groups<kFp8, RW, NG, (DW == 16 ? (kFp8 ? 2 : 1) : 4) / (kFp8 ? 2 : 1)>(
-          stage + wid * stage_bytes(kMaxNB), wb, woff, wrow, hb, hoff, sc, sc, s0, s1 - s0, rot, acc);
+      dot_steps_groups<kFp8, RW, NG, DW == 16 ? 1 : (kFp8 ? 2 : 4)>(
+          my_stage, wb, woff, wrow, hb, hoff, sc, sc, s0, s1 - s0, rot, acc);
 #pragma unroll
       for (int q = 0; q < NG; ++q)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) add(first + q * kGroup + 16 * t, acc[q][t], true);
+        for (int t = 0; t < 2; ++t) add(word, first + q * kGroup + 16 * t, acc[q][t], true);
     };
-    if (kMaxNB == 1 || cnt <= 8) {
-      pass(std::integral_constant<int, 1>{});
-    } else if constexpr (kMaxNB > 1) {
+    if constexpr (kMaxNB > 1) {
       if (cnt <= 16) pass(std::integral_constant<int, 2>{});
       else if (cnt <= kGroup) pass(std::integral_constant<int, 4>{});
       else if (DW == 8 && parts == 4) groups(std::integral_constant<int, DW == 8 ? 4 : 2>{}, 0);
