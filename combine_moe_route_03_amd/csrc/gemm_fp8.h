@@ -25,6 +25,11 @@ __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
 }
 
+// A block barrier behind this wave's LDS operations, not its loads.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 struct Tile {
   int e, row0, rows, ntile;  // e < 0: no tile for this block
 };

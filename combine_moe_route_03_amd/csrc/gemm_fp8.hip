@@ -106,11 +106,6 @@ __device__ __forceinline__ Tile tile_at_place(const int* pre, const int32_t* __r
   return {ok ? e : -1, ok ? (int)first : 0, ok ? rows : 0, ntile};
 }
 
-// A block barrier behind this wave's LDS operations, not its loads.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // Block tiles of BM x BN by WM x WN waves, each wave BM/WM x BN/WN as MI x NI
 // fragments of 16 x 16; the wave's row fragments are 16 WM rows apart, so the waves
 // share the rows of a partial tile evenly, and tiles of up to a quarter or a half of

@@ -7,14 +7,16 @@
 // its L2: those tiles load them cached, all others past the caches (128 experts, N
 // 2816, K 4096, 128 tokens most of whose picks go to 8 experts: 243 us with every
 // load past the caches, 211 with the cached ones for 17 to 32 rows of any expert,
-// 198 = 6.2 TB/s as it is, 6.3 TB/s with even routing; memory reads 1.48, 1.37 and
+// 198 = 6.2 TB/s as it is, 6.4 TB/s with even routing; memory reads 1.48, 1.37 and
 // 1.33 GB for 1.23 GB of weights).
 //
 // A wave computes 32 weight rows by up to 32 tokens (two fragments of 16 rows, so
 // that a token fragment is loaded once for both), one
 // v_mfma_f32_16x16x128_f8f6f4 a K step of 128, 16 rows and 16 tokens, folded with
 // the two scales into fp32 as in gemm_fp8.hip. The tile's row scales are kept in
-// LDS: read from memory a step at a time they cost 7-18% (16 lines a load).
+// LDS: read from memory a step at a time they cost 7-18% (16 lines a load). They are
+// requested before the first steps' weights and put there behind them (the weights
+// only after that: 2-4% more, N 4096, K 1408, even routing 125 against 122 us).
 #include <type_traits>
 
 #include "device.h"
@@ -44,13 +46,15 @@ constexpr int kRing = NB == 4 ? 2 : 3;
 // chunk, wrow their LDS rows in the fragment; xoff[b]: in xb of its token of
 // group b at its chunk (kOutside: none); ss: row scales [kRows][kSPitch] of these
 // steps; c0, c1: weight scales of D registers 0-1 and 2-3, lane l's of step s0 + l.
-// kShared: other blocks read these weights.
-template <bool kTwoScales, int NB, bool kShared>
+// kShared: other blocks read these weights. settle: called when the first loads are
+// on their way; ss, c0 and c1 are there when it returns.
+template <bool kTwoScales, int NB, bool kShared, typename Settle>
 __device__ __forceinline__ void dot_steps8(uint8_t* stage, const Buffer& wb,
                                            const uint32_t (&woff)[4], const int (&wrow)[2],
                                            const Buffer& xb, const uint32_t (&xoff)[NB],
-                                           const float* ss, float c0, float c1, int s0, int n,
-                                           int rot, f32x4 (&acc)[2][(NB + 1) / 2]) {
+                                           const float* ss, const float& c0, const float& c1,
+                                           int s0, int n, int rot, f32x4 (&acc)[2][(NB + 1) / 2],
+                                           const Settle& settle) {
   constexpr int NTL = (NB + 1) / 2, D = kRing<NB>;
   const int lane = threadIdx.x & (kWave - 1);
   const int lr = lane >> 3, lc = lane & 7, i = lane & 15, g = lane >> 4;
@@ -103,6 +107,7 @@ __device__ __forceinline__ void dot_steps8(uint8_t* stage, const Buffer& wb,
   };
 #pragma unroll
   for (int u = 0; u < D; ++u) load(u, u);
+  settle();
   for (int q = 0; q < n; q += D) {
 #pragma unroll
     for (int u = 0; u < D; ++u) {
@@ -169,20 +174,30 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_fp8_stream_kernel(
     for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int t = 0; t < NTL; ++t) acc[f][t] = f32x4{0, 0, 0, 0};
+    constexpr int kThreads = kWave * kWaves, kPer = kRows * kChunk / kThreads;
     for (int s0 = 0; s0 < KB; s0 += kChunk) {
       const int n = KB - s0 < kChunk ? KB - s0 : kChunk;
+      // the scales first, then the first steps' loads, which do not wait for them
       const int l = s0 + (lane < n ? lane : 0);
       float c0 = bs0[l], c1 = bs1[l];
-      // landed here: a use inside the step loop would wait for the ring's loads too
-      asm volatile("" : "+v"(c0), "+v"(c1));
-      if (s0 > 0) __syncthreads();
-      for (int q = tid; q < kRows * kChunk; q += kWave * kWaves) {
-        const int r = q / kChunk, k = q % kChunk;
-        ss[r * kSPitch + k] = r < rows && k < n ? Asc[(int64_t)(row0 + r) * KB + s0 + k] : 0.f;
+      float sc[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int r = tid / kChunk + j * (kThreads / kChunk), k = tid % kChunk;
+        sc[j] = r < rows && k < n ? Asc[(int64_t)(row0 + r) * KB + s0 + k] : 0.f;
       }
-      __syncthreads();
-      dot_steps8<kGateUp, NB, decltype(shared)::value>(stage[wid], wb, woff, wrow, xb, xoff, ss, c0, c1, s0, n,
-                              (tile.ntile + row0) * 5 % n, acc);
+      const auto settle = [&]() __attribute__((always_inline)) {
+        // landed here: a use inside the step loop would wait for the ring's loads too
+        asm volatile("" : "+v"(c0), "+v"(c1));
+        if (s0 > 0) lds_barrier();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          ss[(tid / kChunk + j * (kThreads / kChunk)) * kSPitch + tid % kChunk] = sc[j];
+        lds_barrier();
+      };
+      dot_steps8<kGateUp, NB, decltype(shared)::value>(stage[wid], wb, woff, wrow, xb, xoff, ss, c0,
+                                                       c1, s0, n, (tile.ntile + row0) * 5 % n, acc,
+                                                       settle);
     }
     if constexpr (kGateUp) {
       __syncthreads();  // every wave is done with its stage

@@ -183,7 +183,7 @@ def test_expert_gemm_fp8_buckets_outside_the_rows_are_ignored():
 
 
 def test_expert_gemm_fp8_bad_buckets_among_many_rows():
-    """The same with more rows than 24 an expert: counts and offsets that leave the rows."""
+    """The same with many rows an expert: counts and offsets that leave the rows."""
     c = torch.tensor([130, 100, 7, 5000], dtype=torch.int32, device=DEV)
     o = torch.tensor([10, 250, -2, 0], dtype=torch.int32, device=DEV)  # only the first lies inside
     a, sa = moe.quantize(randn(300, 256, seed=1).to(DEV))
