@@ -16,6 +16,12 @@
 // weights are the first operand: a lane then holds four outputs of ONE row m
 // (n = 4 (lane / 16) + 0..3, m = lane % 16), so the row scale is one register
 // a lane, the weight scale is uniform, and stores are 16 bytes a lane.
+//
+// Bound by the K loop: 8192 x 4096 x 7168 takes 200-227 us, 2.1-2.4 PFLOP/s, the
+// matrix pipes 51% busy; timing-only copies without the loads into LDS 178 of 229
+// us, without loads and folds 153, the matrix instructions alone would take 109.
+// The FFN of 16384 rows, 16 experts, H 4096, I 1408: 365 us (gate/up 244, down
+// 122), 1.55 PFLOP/s.
 #include <type_traits>
 
 #include "device.h"
