@@ -756,6 +756,9 @@ int check_gemm_fp8_sizes(int64_t rows, int64_t E, int64_t N, int64_t K) {
   if (E * N * K >= (int64_t(1) << 40)) return MOE_ERR_ARG;
   const int64_t mtiles = rows / 32 + (rows < E ? rows : E);
   if (mtiles * ceil_div(N, 128) >= (int64_t(1) << 30)) return MOE_ERR_ARG;
+  // one K step: a block of 512 threads for each tile of 32 rows, in a grid of less than
+  // 2^32 threads (longer K has so many tiles only in the persistent kernel)
+  if (K == 128 && mtiles * ceil_div(N, 256) >= (int64_t(1) << 23) - 64) return MOE_ERR_ARG;
   return MOE_OK;
 }
 
@@ -786,6 +789,10 @@ int moe_quantize(const void* x, int32_t dtype, int32_t batch, int32_t rows, int3
   // 16-byte vectors are counted in 32 bits
   const int64_t vecs = (dtype == MOE_BF16 ? 16 : 32) * ceil_div(cols, 128);
   if (int64_t(batch) * rows >= kIndexLimit || int64_t(batch) * rows * vecs >= kIndexLimit)
+    return MOE_ERR_ARG;
+  // a block of 256 threads for each of the weights', in a grid of less than 2^32 threads
+  if (block_rows == 128 &&
+      batch * ceil_div(rows, 128) * ceil_div(cols, 128) >= (int64_t(1) << 24))
     return MOE_ERR_ARG;
   if (batch > 0 && rows > 0 && (!x || !q || !scale)) return MOE_ERR_ARG;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_ALIGN;

@@ -331,8 +331,8 @@ int moe_expert_swiglu(const moe_shape* shape, int32_t I, const void* send_buf,
  * magnitude, scale = 2^p with the smallest p >= -126 for which amax <= 448 * 2^p
  * (1 when amax is 0), q = x * 2^-p rounded once to e4m3 (nearest, ties to even);
  * infinities saturate to +-448, NaN stays NaN.
- * cols % 16 == 0; batch * rows * ceil(cols/128) < 2^27 for bf16, 2^26 for fp32; x and
- * q 16-byte aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also cols % 16),
+ * cols % 16 == 0; batch * rows * ceil(cols/128) < 2^27 for bf16, 2^26 for fp32;
+ * fewer than 2^24 blocks of 128 rows; x and q 16-byte aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also cols % 16),
  * MOE_ERR_UNSUPPORTED (dtype), MOE_ERR_DEVICE. */
 int moe_quantize(const void* x, int32_t dtype, int32_t batch, int32_t rows, int32_t cols,
                  int32_t block_rows, void* q, float* scale, moe_stream_t stream);
@@ -358,7 +358,9 @@ int moe_dispatch_copy_fp8(const moe_shape* shape, const void* x, const int32_t* 
  * overlap; one that does not lie in [0, rows) gives no output.
  * a [rows][K], w [E][N][K] e4m3, a_scale [rows][K/128], w_scale
  * [E][ceil(N/128)][K/128] fp32, out [rows][N] bf16. K % 128 == 0, N % 16 == 0,
- * 1 <= E <= 1024, N*K < 2^31, 256*K < 2^31, 512*N < 2^31; a, w, out 16-byte aligned.
+ * 1 <= E <= 1024, N*K < 2^31, 256*K < 2^31, 512*N < 2^31, E*N*K < 2^40, fewer than
+ * 2^30 tiles of 32 rows (+ min(rows, E)) by 128 columns, with K = 128 fewer than
+ * 2^23 - 64 by 256; a, w, out 16-byte aligned.
  * One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_DEVICE. */
 int moe_expert_gemm_fp8(int32_t rows, int32_t E, int32_t N, int32_t K, const void* a,
                         const float* a_scale, const int32_t* expert_offsets,

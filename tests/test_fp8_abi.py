@@ -42,6 +42,16 @@ def test_quantize_refusals(kw, status):
     assert moe.lib().moe_quantize(*a.values(), None) == status
 
 
+def test_sizes_beyond_a_grid_are_refused():
+    """Grids hold less than 2^32 threads: what would need more is refused, not half launched."""
+    L = moe.lib()
+    assert L.moe_quantize(FAKE, 1, 1 << 19, 1, 4096, 128, FAKE, FAKE, None) == ARG
+    assert L.moe_quantize(FAKE, 1, 1 << 24, 1, 128, 128, FAKE, FAKE, None) == ARG
+    args = (FAKE,) * 7 + (None,)
+    assert L.moe_expert_gemm_fp8(1 << 24, 1, 4096, 128, *args) == ARG
+    assert L.moe_expert_gemm_fp8(1 << 28, 1, 256, 128, *args) == ARG
+
+
 def test_quantize_nothing():
     assert moe.lib().moe_quantize(None, 1, 0, 4, 128, 1, None, None, None) == OK
     assert moe.lib().moe_quantize(None, 0, 3, 0, 128, 128, None, None, None) == OK

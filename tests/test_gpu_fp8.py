@@ -238,6 +238,53 @@ def test_without_rows():
     assert bool((out == 4.0).all())
 
 
+def e4m3_bytes(*shape, seed):
+    """Random e4m3 values made on the device (no NaN)."""
+    g = torch.Generator(DEV).manual_seed(seed)
+    b = torch.randint(0, 240, shape, dtype=torch.uint8, device=DEV, generator=g)
+    b.bitwise_xor_((b & 1) << 7)  # signs
+    return b.bitwise_and_(0xF7).view(F8)
+
+
+def test_rows_and_weights_past_32_bits():
+    """More than 2^32 bytes of rows, of weights and of send rows: the last ones as alone."""
+    K, N, n = 2048, 32, 300
+    rows = (1 << 32) // K + 5000
+    a = e4m3_bytes(rows, K, seed=1)
+    sa = torch.rand(rows, K // 128, device=DEV) + 0.5
+    w, sw = [t.to(DEV) for t in fp8_weights(1, N, K, 3)]
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    out = moe.expert_gemm_fp8(a, sa, i32(0), i32(rows), w, sw)
+    alone = moe.expert_gemm_fp8(a[-n:], sa[-n:], i32(0), i32(n), w, sw)
+    assert torch.equal(out[-n:], alone)
+    del a, sa, out
+    E, N = 520, 4096
+    w = e4m3_bytes(E, N, K, seed=2)
+    sw = torch.rand(E, N // 128, K // 128, device=DEV) + 0.5
+    for n in (7, 40):  # streamed, and (all the rows in one bucket of many) tiled
+        rows = n if n == 7 else 28 * E + 256
+        a, sa = moe.quantize(randn(rows, K, seed=4).to(DEV))
+        o, c = torch.zeros(E, dtype=torch.int32, device=DEV), torch.zeros(E, dtype=torch.int32, device=DEV)
+        c[-1] = n
+        out = torch.zeros(rows, N, dtype=torch.bfloat16, device=DEV)
+        moe.expert_gemm_fp8(a, sa, o, c, w, sw, out=out)
+        a1 = a[:rows if n == 7 else 300].contiguous()
+        alone = torch.zeros(len(a1), N, dtype=torch.bfloat16, device=DEV)
+        moe.expert_gemm_fp8(a1, sa[:len(a1)].contiguous(), o[-1:], c[-1:], w[-1:].contiguous(),
+                            sw[-1:].contiguous(), out=alone)
+        assert torch.equal(out[:n], alone[:n]) and not bool((out[:n] == 0).all())
+        assert not bool(out[n:].any())
+    del w, sw
+    shape = moe.Shape(70000, 8192, 8, 8, 1, 1, torch.bfloat16)
+    x = torch.randn(shape.T, shape.H, dtype=torch.bfloat16, device=DEV)
+    pos = torch.arange(shape.T * 8, dtype=torch.int32, device=DEV).view(-1, 8).flip(0).contiguous()
+    q, s = moe.dispatch_copy_fp8(x, pos, shape)
+    xq, xs = moe.quantize(x)
+    for t in (0, 1, shape.T // 2, shape.T - 1):
+        for r in pos[t].tolist():
+            assert torch.equal(q[r].view(torch.uint8), xq[t].view(torch.uint8)) and torch.equal(s[r], xs[t])
+
+
 # ------------------------------------------------------------------ FFN
 
 @pytest.mark.parametrize("counts,H,I", [

@@ -109,6 +109,36 @@ def test_layer_zero_tokens():
 
 
 @pytest.mark.parametrize("T", [3, 40])
+def test_layer_weights_past_32_bits(T):
+    """A token's experts lie more than 2^32 bytes into the weights: y is that of a layer
+    of these experts alone."""
+    E, H, I, k, n = 200, 4096, 1408, 4, 8
+    g = torch.Generator(DEV).manual_seed(9)
+    wg, wd = [torch.empty(s, dtype=torch.bfloat16, device=DEV).normal_(std=0.05, generator=g)
+              for s in ((E, 2 * I, H), (E, H, I))]
+    logits = torch.randn(T, E, device=DEV, generator=g)
+    logits[:, -n:] += 50
+    x = randn(T, H, seed=6).to(torch.bfloat16).to(DEV)
+    y, idx, gate = moe.layer(logits, x, k, wg, wd)
+    y1, idx1, gate1 = moe.layer(logits[:, -n:].contiguous(), x, k, wg[-n:], wd[-n:])
+    assert torch.equal(idx, idx1 + E - n) and torch.equal(gate, gate1)
+    assert torch.equal(y, y1) and bool(y.float().norm() > 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [4, 60, 128])
+def test_layer_nan_stays_in_its_token(T, fp8):
+    H, E, k, I = 256, 6, 3, 128
+    w, _, _ = weights(E, H, I, fp8)
+    logits, x = logits_of(T, E, k, "iid"), randn(T, H, seed=6).to(torch.bfloat16)
+    clean, _, _ = call(logits, x, k, w)
+    x[T // 2, 7] = float("nan")
+    y, _, _ = call(logits, x, k, w)
+    keep = torch.arange(T, device=DEV) != T // 2
+    assert bool(y[T // 2].isnan().all()) and torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [3, 40])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_layer_repeats_streams_and_graphs(T, fp8):
     """The same bits from every call (the sums have a fixed order), on another
