@@ -17,11 +17,11 @@
 // (n = 4 (lane / 16) + 0..3, m = lane % 16), so the row scale is one register
 // a lane, the weight scale is uniform, and stores are 16 bytes a lane.
 //
-// Bound by the K loop: 8192 x 4096 x 7168 takes 200-227 us, 2.1-2.4 PFLOP/s, the
-// matrix pipes 51% busy; timing-only copies without the loads into LDS 178 of 229
-// us, without loads and folds 153, the matrix instructions alone would take 109.
-// The FFN of 16384 rows, 16 experts, H 4096, I 1408: 365 us (gate/up 244, down
-// 122), 1.55 PFLOP/s.
+// Bound by the K loop: 8192 x 4096 x 7168 takes 197-209 us, 2.3-2.4 PFLOP/s, the
+// matrix pipes 55% busy; timing-only copies without the loads into LDS 50 us less,
+// without loads and folds 75, the matrix instructions alone would take 109.
+// The FFN of 16384 rows, 16 experts, H 4096, I 1408: 360 us (gate/up 244, down
+// 120), 1.57 PFLOP/s.
 #include <type_traits>
 
 #include "device.h"
@@ -121,7 +121,9 @@ __device__ __forceinline__ Tile tile_at_place(const int* pre, const int32_t* __r
 // weights), and the K steps of its tiles are one stream: the loads run two steps
 // ahead, into the next tile's first steps while this one's last run and its results are
 // stored. The tiles of an XCD's last, partial round are cut into two or four by
-// rows where that still gives each unit one.
+// rows where that still gives each unit one, and come first: blocks then end their
+// tiles, and store, at different times (24558 rows of 64 experts, N 2048, K 1408:
+// 118 us with them last, 114 so).
 template <bool kGateUp, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ Asc,
@@ -158,16 +160,17 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   const int mine = total - first < per ? total - first : per;  // the XCD's tiles
   const int whole = mine > 0 ? mine / hop * hop : 0, rest = mine - whole;
   const int cut = rest * 4 <= hop ? 4 : (rest * 2 <= hop ? 2 : 1);
-  const int limit = whole + rest * cut;
   int place = blockIdx.x / kXCD;
+  const bool begins = place < rest * cut;  // with a part of a tile; then the whole rounds
+  const int limit = begins ? whole + hop : whole;
   if (mine <= 0 || place >= limit) return;  // uniform over the block
   const auto tile_of = [&](int p) {
     if (p >= limit) return Tile{-1, 0, 0, 0};
-    const int q = p - whole;  // past the whole rounds: part q % cut of a tile
+    const bool part = begins && p < hop;
     Tile t = tile_at_place<BM>(pre, offs, cnts, E, rows_total, ntiles,
-                               first + (q < 0 ? p : whole + q / cut));
-    if (q >= 0 && cut > 1 && t.e >= 0) {
-      const int r0 = q % cut * (BM / cut), left = t.rows - r0;
+                               first + (part ? whole + p / cut : begins ? p - hop : p));
+    if (part && cut > 1 && t.e >= 0) {
+      const int r0 = p % cut * (BM / cut), left = t.rows - r0;
       t.rows = left < BM / cut ? left : BM / cut;
       t.row0 += r0;
       if (left <= 0) t = {-1, 0, 0, 0};
@@ -379,17 +382,37 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
     if constexpr (!kGateUp) {
       const __amdgpu_buffer_rsrc_t crsrc = make_rsrc(
           static_cast<uint16_t*>(C) + (int64_t)tile.row0 * N, (int64_t)tile.rows * N * 2);
+      // Lanes 8 apart swap halves, so that one store is 8 rows of whole 128-byte lines
+      // instead of 16 rows of half ones, and the lines go past the caches, which keep
+      // operands (8192 x 4096 x 7168: 215 us, cached whole lines 212, so 198; 24558
+      // rows, N 2048, K 1408: 113, 110 and 108; without any stores 195 and 89).
+      const bool low = (lane & 8) == 0;
+      const int row = wm * 16 + (fi & 7);
 #pragma unroll
-      for (int p = 0; p < NI / 2; ++p) {
-        const int n = ncol + 32 * p + 8 * g;
+      for (int p = 0; p < NI / 2; p += 2) {
+        const int n = ncol + 32 * p + 8 * g + (low ? 0 : 32);
 #pragma unroll
         for (int mi = 0; mi < ML; ++mi) {
-          const f32x4 lo = acc[2 * p][mi], hi = acc[2 * p + 1][mi];
-          const v4u v = {bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]),
-                         bf16x2_rne(hi[0], hi[1]), bf16x2_rne(hi[2], hi[3])};
+          v4u v[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const f32x4 lo = acc[2 * (p + q)][mi], hi = acc[2 * (p + q) + 1][mi];
+            v[q] = v4u{bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]),
+                       bf16x2_rne(hi[0], hi[1]), bf16x2_rne(hi[2], hi[3])};
+          }
+          v4u top, bottom;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t give = low ? v[1][j] : v[0][j];
+            const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0x128, 0xF, 0xF, true);
+            top[j] = low ? v[0][j] : got;
+            bottom[j] = low ? got : v[1][j];
+          }
           // columns past N would wrap into the next row: offset out of range instead
-          const uint32_t off = n < N ? ((uint32_t)(arow + mi * kFragRows) * (uint32_t)N + n) * 2 : kOutside;
-          __builtin_amdgcn_raw_buffer_store_b128(v, crsrc, off, 0, 0);
+          const uint32_t at = ((uint32_t)(row + mi * kFragRows) * (uint32_t)N + n) * 2;
+          __builtin_amdgcn_raw_buffer_store_b128(top, crsrc, n < N ? at : kOutside, 0, kStream);
+          __builtin_amdgcn_raw_buffer_store_b128(bottom, crsrc, n < N ? at + 16 * (uint32_t)N : kOutside,
+                                                 0, kStream);
         }
       }
     } else {
