@@ -37,15 +37,12 @@ struct Buffer {
   }
 };
 
-// 16 or 4 bytes at off + step (step uniform).
+// 16 bytes at off + step (step uniform).
 __device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, step, 0);
 }
 __device__ __forceinline__ v4u load16_stream(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, step, kStream);
-}
-__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step) {
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, step, 0));
 }
 
 // Byte offset of 16-byte chunk c of LDS tile row r (rows of 128 bytes): the 16
