@@ -34,13 +34,26 @@ struct Tile {
   int e, row0, rows, ntile;  // e < 0: no tile for this block
 };
 
+// Row tiles of a bucket: none for one that does not lie in [0, rows_total), so that what
+// it claims takes no place in a list that is sized for buckets that do.
+template <int BM>
+__device__ __forceinline__ int bucket_tiles(int off, int n, int64_t rows_total) {
+  return n > 0 && off >= 0 && (int64_t)off + n <= rows_total ? (n - 1) / BM + 1 : 0;
+}
+// Most row tiles of buckets that do not overlap. Lists end there, so that any offsets and
+// counts make a bounded list (and 64 lanes' shares, each cut to it, an int).
+template <int BM>
+__device__ __forceinline__ int most_tiles(int E, int64_t rows_total) {
+  return (int)(rows_total / BM + (rows_total < E ? rows_total : E));
+}
+
 // Block -> tile, for tiles that share weights with their neighbours at most. The
 // tiles of all experts, in patches of kGroupM m-tiles by all n-tiles, form one list;
 // workgroups are dealt to the 8 XCDs round-robin and each XCD takes every eighth
 // run of kGroupM tiles: the m-tiles of a long expert read the same weights through
 // one L2, and the long experts' tiles, which take longer, spread over the XCDs
-// (contiguous shares: decode product with hot experts 243 us). Counts that leave [0,
-// rows_total) give no tile. Called by the whole block; info: 4 ints of LDS.
+// (contiguous shares: decode product with hot experts 243 us). Called by the whole
+// block; info: 4 ints of LDS.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offs,
                                           const int32_t* __restrict__ cnts, int E,
@@ -50,18 +63,17 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offs,
     if (lane == 0) info[0] = -1;
     const int c = (E + kWave - 1) / kWave;  // lane l scans experts [l*c, l*c + c)
     const int e0 = lane * c, e1 = (e0 + c < E) ? e0 + c : E;
-    const auto mtiles = [&](int e) {
-      const int n = cnts[e];
-      return n > 0 && n <= rows_total ? (n - 1) / BM + 1 : 0;
-    };
+    const int most = most_tiles<BM>(E, rows_total);
+    const auto mtiles = [&](int e) { return bucket_tiles<BM>(offs[e], cnts[e], rows_total); };
     int mine = 0;
     for (int e = e0; e < e1; ++e) mine += mtiles(e);
+    mine = mine < most ? mine : most;
     int incl = mine;
     for (int o = 1; o < kWave; o <<= 1) {
       const int y = __shfl_up(incl, o);
       if (lane >= o) incl += y;
     }
-    const int MT = __shfl(incl, kWave - 1);
+    const int all = __shfl(incl, kWave - 1), MT = all < most ? all : most;
     const int total = MT * ntiles;
     const int slot = blockIdx.x / kXCD;
     const int lin = ((slot / kGroupM) * kXCD + blockIdx.x % kXCD) * kGroupM + slot % kGroupM;
@@ -76,13 +88,10 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offs,
           if (mt < base + n) {
             const int m0 = (mt - base) * BM;
             const int rows = cnts[e] - m0;
-            const int64_t first = (int64_t)offs[e] + m0;
-            if (first >= 0 && first + (rows < BM ? rows : BM) <= rows_total) {
-              info[0] = e;
-              info[1] = (int)first;
-              info[2] = rows < BM ? rows : BM;
-              info[3] = ntile;
-            }
+            info[0] = e;
+            info[1] = offs[e] + m0;
+            info[2] = rows < BM ? rows : BM;
+            info[3] = ntile;
             break;
           }
           base += n;

@@ -56,21 +56,19 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* lds
 }
 
 // m-tile prefix sums of the experts in LDS: pre[e] m-tiles before expert e, pre[E] in
-// all. Counts outside [0, rows_total] give no tile, and the list ends with as many
-// tiles as buckets that do not overlap can have, so that any counts make a
-// bounded list. Called by the whole block.
+// all (gemm_fp8.h says which buckets count). Called by the whole block.
 template <int BM>
-__device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ cnts, int E,
+__device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ offs,
+                                            const int32_t* __restrict__ cnts, int E,
                                             int64_t rows_total, int* pre) {
   if (threadIdx.x < kWave) {
     const int lane = threadIdx.x;
     const int c = (E + kWave - 1) / kWave;  // lane l scans experts [l*c, l*c + c)
     const int e0 = lane * c, e1 = (e0 + c < E) ? e0 + c : E;
-    const int most = (int)(rows_total / BM + (rows_total < E ? rows_total : E));
+    const int most = most_tiles<BM>(E, rows_total);
     int mine = 0;
     for (int e = e0; e < e1; ++e) {
-      const int n = cnts[e];
-      mine += n > 0 && n <= rows_total ? (n - 1) / BM + 1 : 0;
+      mine += bucket_tiles<BM>(offs[e], cnts[e], rows_total);
       pre[e + 1] = mine;
     }
     mine = mine < most ? mine : most;
@@ -88,12 +86,12 @@ __device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ cnts, in
   __syncthreads();
 }
 
-// Tile number lin of the list (patches of kGroupM m-tiles by all n-tiles); e < 0
-// where the expert's rows do not lie in [0, rows_total). Uniform, no barrier.
+// Tile number lin of the list (patches of kGroupM m-tiles by all n-tiles). Uniform, no
+// barrier.
 template <int BM>
 __device__ __forceinline__ Tile tile_at_place(const int* pre, const int32_t* __restrict__ offs,
                                               const int32_t* __restrict__ cnts, int E,
-                                              int64_t rows_total, int ntiles, int lin) {
+                                              int ntiles, int lin) {
   const int lane = threadIdx.x & (kWave - 1);
   const int MT = __builtin_amdgcn_readfirstlane(pre[E]);
   const int grp = lin / (kGroupM * ntiles), r = lin - grp * kGroupM * ntiles;
@@ -106,10 +104,8 @@ __device__ __forceinline__ Tile tile_at_place(const int* pre, const int32_t* __r
   const int at = part * c + 1 + lane;
   const int e = part * c + __popcll(__ballot(lane < c && at <= E && pre[at < E ? at : E] <= mt));
   const int m0 = (mt - __builtin_amdgcn_readfirstlane(pre[e])) * BM;
-  const int left = cnts[e] - m0, rows = left < BM ? left : BM;
-  const int64_t first = (int64_t)offs[e] + m0;
-  const bool ok = first >= 0 && first + rows <= rows_total;
-  return {ok ? e : -1, ok ? (int)first : 0, ok ? rows : 0, ntile};
+  const int left = cnts[e] - m0;
+  return {e, offs[e] + m0, left < BM ? left : BM, ntile};
 }
 
 // Block tiles of BM x BN by WM x WN waves, each wave BM/WM x BN/WN as MI x NI
@@ -152,7 +148,7 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   const int KB = K / kBK, I = N / 2, NB = (N + kQuantBlock - 1) / kQuantBlock;
 
   // ---- the block's tiles: places place, place + hop, ... below limit
-  tile_prefix<BM>(cnts, E, rows_total, pre);
+  tile_prefix<BM>(offs, cnts, E, rows_total, pre);
   const int total = __builtin_amdgcn_readfirstlane(pre[E]) * ntiles;
   const int per = (total + kXCD - 1) / kXCD;
   const int hop = gridDim.x / kXCD;
@@ -167,9 +163,9 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_fp8_kernel(
   const auto tile_of = [&](int p) {
     if (p >= limit) return Tile{-1, 0, 0, 0};
     const bool part = begins && p < hop;
-    Tile t = tile_at_place<BM>(pre, offs, cnts, E, rows_total, ntiles,
+    Tile t = tile_at_place<BM>(pre, offs, cnts, E, ntiles,
                                first + (part ? whole + p / cut : begins ? p - hop : p));
-    if (part && cut > 1 && t.e >= 0) {
+    if (part && cut > 1) {
       const int r0 = p % cut * (BM / cut), left = t.rows - r0;
       t.rows = left < BM / cut ? left : BM / cut;
       t.row0 += r0;
