@@ -27,8 +27,9 @@ constexpr uint32_t kOutside = 0x80000000u;
 constexpr int kStream = 2;  // cache policy: weights are read once
 
 // A buffer whose loads can be switched off: past the last step of a stream its
-// descriptor is empty (and the step 0, whatever the order in which the range check
-// subtracts it), so the loop needs neither branches nor address selects.
+// descriptor is empty, so the loop needs neither branches nor address selects. The
+// scalar offset (step) has to be 0 then: the range check takes it from the
+// descriptor's size, and with more the difference could wrap and let every lane in.
 struct Buffer {
   const void* base;
   uint32_t bytes;
