@@ -754,11 +754,13 @@ int check_gemm_fp8_sizes(int64_t rows, int64_t E, int64_t N, int64_t K) {
   if (N * K >= (int64_t(1) << 31) || 256 * K >= (int64_t(1) << 31) || 512 * N >= (int64_t(1) << 31))
     return MOE_ERR_ARG;
   if (E * N * K >= (int64_t(1) << 40)) return MOE_ERR_ARG;
-  const int64_t mtiles = rows / 32 + (rows < E ? rows : E);
+  const int64_t mtiles = rows / moe::kStreamRows + (rows < E ? rows : E);
   if (mtiles * ceil_div(N, 128) >= (int64_t(1) << 30)) return MOE_ERR_ARG;
-  // one K step: a block of 512 threads for each tile of 32 rows, in a grid of less than
-  // 2^32 threads (longer K has so many tiles only in the persistent kernel)
-  if (K == 128 && mtiles * ceil_div(N, 256) >= (int64_t(1) << 23) - 64) return MOE_ERR_ARG;
+  // the streamed kernel has a block for each tile, in a grid of less than 2^32 threads
+  // (the other one's grid has one for each compute unit)
+  if (moe::gemm_fp8_streams(rows, E, K) &&
+      mtiles * ceil_div(N, moe::kStreamCols) >= (int64_t(1) << 32) / moe::kStreamThreads - 64)
+    return MOE_ERR_ARG;
   return MOE_OK;
 }
 

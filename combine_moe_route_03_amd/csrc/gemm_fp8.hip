@@ -521,23 +521,13 @@ hipError_t run_gemm(const void* a, const float* asc, int64_t rows, int E, const 
                 rows, static_cast<const uint8_t*>(w), wsc, N, K, c, csc, ntiles);
 }
 
-// Rows an expert on average up to which the streamed products (tiles of 32 rows)
-// are the faster. 128 experts, N 2816, K 4096, even routing: 16 rows 258 against
-// 318 us, 24 rows 283 against 321, 28 rows 316 against 326, 32 rows (half the
-// experts take two tiles) 343 against 328; N 4096, K 1408: 16 rows 140 against
-// 159, 28 rows 163 against 166, 32 rows 181 against 168. Most picks on 8 experts,
-// N 2816: 8 rows 198 against 264, 24 rows 287 against 346.
-// One K step is too short for the tiled kernel's stream of loads.
-constexpr int kFewRows = 28;
-bool few_rows(int64_t rows, int E, int K) { return K == kBK || rows <= (int64_t)kFewRows * E; }
-
 }  // namespace
 
 hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
                            const int32_t* offs, const int32_t* cnts, const void* w,
                            const float* wsc, int N, int K, void* out, hipStream_t s) {
   if (rows == 0) return hipSuccess;
-  if (few_rows(rows, E, K))
+  if (gemm_fp8_streams(rows, E, K))
     return launch_gemm_fp8_stream(false, a, asc, rows, E, offs, cnts, w, wsc, N, K, out, nullptr, s);
   return run_gemm<false, 256, 256, 4, 2>(a, asc, rows, E, offs, cnts, w, wsc, N, K, out, nullptr,
                                             s);
@@ -550,7 +540,7 @@ hipError_t launch_expert_swiglu_fp8(const void* send, const float* ssc, int64_t 
                                     hipStream_t s) {
   if (rows == 0) return hipSuccess;
   const hipError_t err =
-      few_rows(rows, E, H)
+      gemm_fp8_streams(rows, E, H)
           ? launch_gemm_fp8_stream(true, send, ssc, rows, E, offs, cnts, w_gate_up, gsc, 2 * I, H, hq,
                                    hs, s)
           : run_gemm<true, 256, 256, 4, 2>(send, ssc, rows, E, offs, cnts, w_gate_up, gsc, 2 * I,

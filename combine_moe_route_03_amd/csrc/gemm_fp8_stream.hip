@@ -29,8 +29,8 @@
 namespace moe {
 namespace {
 
-constexpr int kRows = 32;    // rows of a tile
-constexpr int kWaves = 8;    // waves of a block
+constexpr int kRows = kStreamRows;  // rows of a tile
+constexpr int kWaves = kStreamThreads / kWave;
 constexpr int kChunk = 64;   // K steps whose scales are held at a time
 constexpr int kSPitch = kChunk + 1;
 
@@ -132,6 +132,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_fp8_stream_kernel(
   constexpr int kNO = kWaves * kWaveCols;  // output columns of a tile
   constexpr int kPitch = kNO + 4;          // floats of an h row in LDS
   static_assert(!kGateUp || kNO == kQuantBlock, "one scale block of h per tile");
+  static_assert(kNO * (kGateUp ? 2 : 1) == kStreamCols, "rows of w a tile");
   __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][kStageBytes];
   __shared__ __attribute__((aligned(16))) float ss[kRows * kSPitch];
   __shared__ int info[4];

@@ -231,6 +231,19 @@ hipError_t launch_dispatch_fp8(const void* x, int dtype, const int32_t* pos, int
 hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
                            const int32_t* offs, const int32_t* cnts, const void* w,
                            const float* wsc, int N, int K, void* out, hipStream_t s);
+// Whether that product (or the gate/up product) streams the weights, in tiles of
+// kStreamRows rows by kStreamCols of the N rows of w. Rows an expert on average up to
+// which that is the faster: 128 experts, N 2816, K 4096, even routing: 16 rows 258 against
+// 318 us, 24 rows 283 against 321, 28 rows 316 against 326, 32 rows (half the
+// experts take two tiles) 343 against 328; N 4096, K 1408: 16 rows 140 against
+// 159, 28 rows 163 against 166, 32 rows 181 against 168. Most picks on 8 experts,
+// N 2816: 8 rows 198 against 264, 24 rows 287 against 346.
+// One K step is too short for the tiled kernel's stream of loads.
+constexpr int kFewRows = 28;
+constexpr int kStreamRows = 32, kStreamCols = 256, kStreamThreads = 512;
+inline bool gemm_fp8_streams(int64_t rows, int64_t E, int64_t K) {
+  return K == 128 || rows <= kFewRows * E;
+}
 // The same (gate_up: with the FFN's epilogue, c = hq, csc = hs, N = 2 I) for few
 // rows an expert: weights streamed, tiles of 32 rows.
 hipError_t launch_gemm_fp8_stream(bool gate_up, const void* a, const float* asc, int64_t rows,

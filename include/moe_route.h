@@ -359,8 +359,8 @@ int moe_dispatch_copy_fp8(const moe_shape* shape, const void* x, const int32_t* 
  * a [rows][K], w [E][N][K] e4m3, a_scale [rows][K/128], w_scale
  * [E][ceil(N/128)][K/128] fp32, out [rows][N] bf16. K % 128 == 0, N % 16 == 0,
  * 1 <= E <= 1024, N*K < 2^31, 256*K < 2^31, 512*N < 2^31, E*N*K < 2^40, fewer than
- * 2^30 tiles of 32 rows (+ min(rows, E)) by 128 columns, with K = 128 fewer than
- * 2^23 - 64 by 256; a, w, out 16-byte aligned.
+ * 2^30 tiles of 32 rows (+ min(rows, E)) by 128 columns, with K = 128 or at most 28 * E
+ * rows fewer than 2^23 - 64 by 256; a, w, out 16-byte aligned.
  * One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_DEVICE. */
 int moe_expert_gemm_fp8(int32_t rows, int32_t E, int32_t N, int32_t K, const void* a,
                         const float* a_scale, const int32_t* expert_offsets,
