@@ -160,6 +160,12 @@ def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p | None:
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _int32(*sizes: int) -> None:
+    """Sizes reach the library as 32-bit integers, which ctypes would cut them to."""
+    if min(sizes) < -(1 << 31) or max(sizes) >= 1 << 31:
+        raise ValueError(f"sizes must fit 32 bits, got {sizes}")
+
+
 @dataclass(frozen=True)
 class Shape:
     T: int
@@ -169,6 +175,9 @@ class Shape:
     R: int
     W: int
     dtype: torch.dtype
+
+    def __post_init__(self):
+        _int32(self.T, self.H, self.E, self.k, self.R, self.W)
 
     def c(self) -> MoeShape:
         return MoeShape(self.T, self.H, self.E, self.k, self.R, self.W, _DTYPE_CODE[self.dtype])
@@ -699,6 +708,7 @@ def quantize(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None = None
     batch = 1
     for n in lead:
         batch *= n
+    _int32(batch, rows, cols)
     sshape = (*lead, -(-rows // block_rows), _blocks(cols))
     q = _empty(shape, _FP8, dev) if q is None else q
     scale = _empty(sshape, torch.float32, dev) if scale is None else scale
@@ -737,6 +747,7 @@ def expert_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: torc
     dev = a.device
     rows, K = a.shape
     E, N, _ = w.shape
+    _int32(rows, E, N, K)
     out = _empty((rows, N), torch.bfloat16, dev) if out is None else out
     f32, i32 = torch.float32, torch.int32
     _check(lib().moe_expert_gemm_fp8(
@@ -751,6 +762,7 @@ def expert_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: torc
 
 
 def expert_swiglu_fp8_workspace_bytes(shape: Shape, I: int) -> int:
+    _int32(I)
     return int(lib().moe_expert_swiglu_fp8_workspace_bytes(ctypes.byref(shape.c()), I))
 
 
@@ -771,6 +783,7 @@ def expert_swiglu_fp8(send_q: torch.Tensor, send_scale: torch.Tensor,
     dev = send_q.device
     E, H, rows = shape.E, shape.H, shape.T * shape.k
     I = w_down.shape[-1]
+    _int32(I)
     f32, i32 = torch.float32, torch.int32
     expert_out = _empty((rows, H), torch.bfloat16, dev) if expert_out is None \
         else expert_out
@@ -791,6 +804,7 @@ def expert_swiglu_fp8(send_q: torch.Tensor, send_scale: torch.Tensor,
 
 
 def layer_workspace_bytes(shape: Shape, I: int) -> int:
+    _int32(I)
     return int(lib().moe_layer_workspace_bytes(ctypes.byref(shape.c()), I))
 
 
@@ -807,6 +821,7 @@ def layer(logits: torch.Tensor, x: torch.Tensor, k: int, w_gate_up: torch.Tensor
         raise ValueError("logits must be [T, E], x [T, H] and w_down [E, H, I]")
     T, E = logits.shape
     H, I = x.shape[1], w_down.shape[2]
+    _int32(T, H, E, k, I)
     f32, bf16 = torch.float32, torch.bfloat16
     fp8 = w_down.dtype == _FP8
     if fp8 and (s_gate_up is None or s_down is None):

@@ -1,9 +1,10 @@
 """Sizes at the limits of the 8-bit entry points, on the CPU: what a kernel cannot count
-is refused. Calls whose sizes pass fail at a later check (a misaligned pointer, a
+is refused, and nothing is cut to 32 bits on the way. Calls whose sizes pass fail at a later check (a misaligned pointer, a
 workspace of no bytes), so that none launches."""
 import ctypes
 
 import pytest
+import torch
 
 import combine_moe_route_03_amd as moe
 from test_abi import ALIGN, ARG, FAKE, WORKSPACE, _shape
@@ -47,3 +48,49 @@ def test_ffn_grids_beyond_32_bits_are_refused():
     assert stream_threads(28 * E, E, 2 * I) >= 1 << 32 and E * 2 * I * H < 1 << 40
     assert ffn(28 * E, E, H, I) == ARG
     assert ffn(28 * E + 1, E, H, I) == WORKSPACE
+
+
+# ------------------------------------------------------------ sizes past 32 bits
+
+BIG = (1 << 32) + 5  # what ctypes would cut to 5
+F8, BF16, F32, I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
+
+
+def meta(*shape, dtype=BF16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("shape", [(BIG, 16), (1 << 16, (1 << 16) + 1, 1, 16), (1, BIG // 16 * 16)])
+def test_quantize_of_more_than_32_bits_of_rows(shape):
+    """The rows, their batches together or the columns."""
+    for block_rows in (1, 128):
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.quantize(meta(*shape), block_rows=block_rows)
+
+
+def test_shapes_of_more_than_32_bits():
+    for name in "THEkRW":
+        kw = dict(T=4, H=128, E=4, k=2, R=1, W=1, dtype=BF16)
+        kw[name] = BIG
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.Shape(**kw)
+
+
+def test_products_and_layers_of_more_than_32_bits():
+    s = moe.Shape(4, 128, 4, 2, 1, 1, BF16)
+    i = meta(4, dtype=I32)
+    for rows, E, N, K in ((BIG, 4, 64, 128), (8, 4, 1 << 33, 128), (8, 4, 64, 1 << 33)):
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.expert_gemm_fp8(meta(rows, K, dtype=F8), meta(rows, K // 128, dtype=F32), i, i,
+                                meta(E, N, K, dtype=F8), meta(E, -(-N // 128), K // 128, dtype=F32))
+    I = 1 << 32
+    wg, wd = meta(4, 2 * I, 128, dtype=F8), meta(4, 128, I, dtype=F8)
+    sg, sd = meta(4, I // 64, 1, dtype=F32), meta(4, 1, I // 128, dtype=F32)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.expert_swiglu_fp8(meta(8, 128, dtype=F8), meta(8, 1, dtype=F32), i, i, s, wg, sg, wd, sd)
+    for f in (moe.expert_swiglu_fp8_workspace_bytes, moe.layer_workspace_bytes):
+        with pytest.raises(ValueError, match="32 bits"):
+            f(s, I + 128)
+    for T, k, inter in ((2, 1, I), (BIG, 1, 128), (0, BIG, 128)):
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.layer(meta(T, 4, dtype=F32), meta(T, 128), k, meta(4, 2 * inter, 128), meta(4, 128, inter))
