@@ -12,8 +12,9 @@
 // v_mfma_f32_16x16x128_f8f6f4 makes one P_b for 16 x 16 outputs in one
 // instruction, started from zero, and the vector unit folds it into the fp32
 // accumulators with one fused multiply-add an output while the next product
-// runs, so any fp32 scales are served (gemm_fp8.h says how exact it is). The
-// weights are the first operand: a lane then holds four outputs of ONE row m
+// runs, so scales need not be powers of two (gemm_fp8.h says how exact the product is).
+// The factor of the fold is sa sw rounded to fp32, hence the range that the header asks
+// of it. The weights are the first operand: a lane then holds four outputs of ONE row m
 // (n = 4 (lane / 16) + 0..3, m = lane % 16), so the row scale is one register
 // a lane, the weight scale is uniform, and stores are 16 bytes a lane.
 //

@@ -321,8 +321,10 @@ int moe_expert_swiglu(const moe_shape* shape, int32_t I, const void* send_buf,
  * finite value 448, no infinity; torch.float8_e4m3fn), one fp32 scale for each
  * block of 128 columns: of one row (tokens, [rows][ceil(cols/128)]) or of 128
  * rows (weights, [ceil(rows/128)][ceil(cols/128)] an expert). A value stands for
- * q * scale. The products take any fp32 scales; the quantisers write powers of
- * two. */
+ * q * scale. The quantisers write powers of two; the products take any finite fp32
+ * scales. They form a_scale * w_scale first, rounded to fp32: it has to stay below 2^128
+ * in magnitude, and where it falls below 2^-126 its rounding costs a result up to
+ * 2^-150 of the sum of |a w|. */
 
 /* Block quantisation of x [batch][rows][cols] (dtype MOE_F32 or MOE_BF16) to q
  * [batch][rows][cols] e4m3 and scale [batch][ceil(rows/block_rows)]
@@ -402,7 +404,8 @@ size_t moe_layer_workspace_bytes(const moe_shape* shape, int32_t I);
  *   y[t][c]    = round_bf16( sum_i topk_w[t][i] sum_j Wd[e][c][j] h[t][i][j] )
  * all sums in fp32 (finite operands as in moe_expert_swiglu). Differs from
  * moe_route + moe_dispatch + moe_expert_swiglu + moe_combine in that the
- * experts' outputs are not rounded to bf16 before they are weighted. Only live
+ * experts' outputs are not rounded to bf16 before they are weighted. 8-bit weights'
+ * scales are finite; a block's product is scaled after its fp32 sum. Only live
  * experts' weights are read, once (w_down twice for an expert with more than 64
  * picks, where H < 4096). Two launches for T <= 8, else one more to route and one more again
  * where a block cannot route all tokens at a time.
