@@ -344,7 +344,8 @@ int moe_quantize(const void* x, int32_t dtype, int32_t batch, int32_t rows, int3
  * row quantisation (moe_quantize, block_rows 1) of x[t]. Each x row is read
  * once; other rows are untouched.
  * x [T][H] (dtype of shape), send_q [T*k][H] e4m3, send_scale
- * [T*k][ceil(H/128)] fp32. H % 16 == 0. Errors: as moe_dispatch_copy. */
+ * [T*k][ceil(H/128)] fp32. H % 16 == 0; T * ceil(H/128) < 2^27 for bf16, 2^26 for
+ * fp32. Errors: as moe_dispatch_copy. */
 int moe_dispatch_copy_fp8(const moe_shape* shape, const void* x, const int32_t* pos, void* send_q,
                           float* send_scale, moe_stream_t stream);
 
@@ -413,7 +414,8 @@ size_t moe_layer_workspace_bytes(const moe_shape* shape, int32_t I);
  * unused (NULL). MOE_F8E4M3: the same in e4m3 with s_gate_up [E][2I/128][H/128],
  * s_down [E][H/128][I/128] fp32; the tokens stay bf16.
  * shape->dtype MOE_BF16 (x and y); R and W only have to be valid. H % 128 == 0,
- * I % 64 == 0 (% 128 with 8-bit weights). logits [T][E] fp32, x and y [T][H],
+ * I % 64 == 0 (% 128 with 8-bit weights); I < 2^20, H < 2^23, 4*I*H < 2^31,
+ * 2*E*I*H < 2^40 (31-bit byte offsets in x, h and one expert's weights). logits [T][E] fp32, x and y [T][H],
  * topk_idx and topk_w [T][k] out. workspace: moe_layer_workspace_bytes(shape, I)
  * bytes, 16-byte aligned, clobbered; calls that overlap need one each.
  * Errors: MOE_ERR_ARG (also T or T * k beyond the limits), MOE_ERR_ALIGN,

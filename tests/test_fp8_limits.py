@@ -50,6 +50,26 @@ def test_ffn_grids_beyond_32_bits_are_refused():
     assert ffn(28 * E + 1, E, H, I) == WORKSPACE
 
 
+def test_dispatch_limits():
+    for dtype, most in ((moe.MOE_BF16, 1 << 27), (moe.MOE_F32, 1 << 26)):
+        for T, H, st in ((most - 1, 16, ALIGN), (most, 16, ARG), (most // 2, 144, ARG)):
+            sh = _shape(T=T, k=1, E=4, H=H, R=1, W=1, dtype=dtype)
+            got = moe.lib().moe_dispatch_copy_fp8(ctypes.byref(sh), FAKE, FAKE, ODD16, FAKE, None)
+            assert got == st, (dtype, T, H)
+
+
+@pytest.mark.parametrize("E,H,I", [
+    (1, 128, (1 << 20) - 64), (1, 128, 1 << 20), (1, (1 << 23) - 128, 64), (1, 1 << 23, 64),
+    (1, 512, (1 << 20) - 64), (1, 1024, 1 << 19), (1, 1024, (1 << 19) - 64), (1024, 1024, 1 << 18),
+    (1023, 1024, (1 << 19) - 64), (1024, 1024, (1 << 19) - 64), (1024, 1152, (1 << 19) - 64), (1, 128, 32)])
+def test_layer_limits(E, H, I):
+    """What the header says of I and H is what is taken."""
+    within = I % 64 == 0 and I < 1 << 20 and H < 1 << 23 and 4 * I * H < 1 << 31 \
+        and 2 * E * I * H < 1 << 40
+    sh = _shape(T=128, k=1, E=E, H=H, R=1, W=1)
+    assert (moe.lib().moe_layer_workspace_bytes(ctypes.byref(sh), I) > 0) == within
+
+
 # ------------------------------------------------------------ sizes past 32 bits
 
 BIG = (1 << 32) + 5  # what ctypes would cut to 5
