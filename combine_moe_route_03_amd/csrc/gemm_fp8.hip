@@ -18,11 +18,12 @@
 // (n = 4 (lane / 16) + 0..3, m = lane % 16), so the row scale is one register
 // a lane, the weight scale is uniform, and stores are 16 bytes a lane.
 //
-// Bound by the K loop: 8192 x 4096 x 7168 takes 197-209 us, 2.3-2.4 PFLOP/s, the
-// matrix pipes 55% busy; timing-only copies without the loads into LDS 50 us less,
-// without loads and folds 75, the matrix instructions alone would take 109.
-// The FFN of 16384 rows, 16 experts, H 4096, I 1408: 360 us (gate/up 244, down
-// 120), 1.57 PFLOP/s.
+// Bound by the K loop: 8192 x 4096 x 7168 takes 196-213 us, 2.3-2.4 PFLOP/s, the
+// matrix pipes 54% busy. Of 229 us, before the results were stored past the caches,
+// timing-only copies took 178 without the loads into LDS, 153 without loads and folds;
+// the matrix instructions alone would take 109.
+// The FFN of 16384 rows, 16 experts, H 4096, I 1408: 353-367 us (gate/up 244, down
+// 120), 1.55-1.6 PFLOP/s.
 #include <type_traits>
 
 #include "device.h"

@@ -238,6 +238,8 @@ hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
 // experts take two tiles) 343 against 328; N 4096, K 1408: 16 rows 140 against
 // 159, 28 rows 163 against 166, 32 rows 181 against 168. Most picks on 8 experts,
 // N 2816: 8 rows 198 against 264, 24 rows 287 against 346.
+// The mean decides since the counts are on the device; one long expert among short
+// ones is streamed too, in its 32-row tiles.
 // One K step is too short for the tiled kernel's stream of loads.
 constexpr int kFewRows = 28;
 constexpr int kStreamRows = 32, kStreamCols = 256, kStreamThreads = 512;

@@ -21,8 +21,8 @@
 // its scale: half the bytes, the same arithmetic on the tokens.
 //
 // Measured (H 4096, I 1408, 128 experts, k 8): one token 277 MB in 54 us (gate/up
-// 36, down 18); 128 tokens on 107 experts, most on 8 of them, 3.69 GB in 600 us,
-// 6.1 TB/s (gate/up 396, down 201); on all 128 experts 4.43 GB in 683 us, 6.5 TB/s.
+// 36, down 18); 128 tokens on 107 experts, most on 8 of them, 3.69 GB in 580-600 us,
+// 6.1-6.3 TB/s (gate/up 385-396, down 193-201); on all 128 experts 4.43 GB in 683 us, 6.5 TB/s.
 #include <type_traits>
 
 #include "device.h"
