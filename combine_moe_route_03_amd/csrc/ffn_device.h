@@ -28,10 +28,10 @@ __device__ __forceinline__ uint32_t bf16x2_rne(float a, float b) {
 // error carried to first order after the exponential), and the reciprocal is
 // the hardware one refined by one Newton step. |g| is cut to 128 for it (e^-128 is
 // zero in fp32 already): the product with log2(e) would overflow from 2.36e38 on, and
-// its error then be NaN. For finite g (minus infinity gives NaN) the relative error is at most 4.6 x 2^-24 against the exact
-// SiLU over 16M arguments in [-100, 100] (3.1 x 2^-24 for expf and an IEEE
-// division), in ~13 instructions instead of ~25: the gate/up epilogue is
-// bound by its instruction count.
+// its error then be NaN. For finite g (minus infinity gives NaN) the relative
+// error is at most 4.6 x 2^-24 against the exact SiLU over 16M arguments in
+// [-100, 100] (3.1 x 2^-24 for expf and an IEEE division), in ~14 instructions
+// instead of ~25: the gate/up epilogue is bound by its instruction count.
 __device__ __forceinline__ float silu(float g) {
   constexpr float kL1 = 1.44269504f;            // log2(e) rounded to float
   constexpr float kL2 = 1.925963033500011e-08f;  // log2(e) - kL1

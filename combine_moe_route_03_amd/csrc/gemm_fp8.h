@@ -41,7 +41,8 @@ __device__ __forceinline__ int bucket_tiles(int off, int n, int64_t rows_total) 
   return n > 0 && off >= 0 && (int64_t)off + n <= rows_total ? (n - 1) / BM + 1 : 0;
 }
 // Most row tiles of buckets that do not overlap. Lists end there, so that any offsets and
-// counts make a bounded list (and 64 lanes' shares, each cut to it, an int).
+// counts make a bounded list. (The entry's limits keep it below 2^23 + 2^10, so 64 lanes'
+// shares, each cut to it, add up in an int.)
 template <int BM>
 __device__ __forceinline__ int most_tiles(int E, int64_t rows_total) {
   return (int)(rows_total / BM + (rows_total < E ? rows_total : E));

@@ -22,7 +22,8 @@
 //
 // Measured (H 4096, I 1408, 128 experts, k 8): one token 277 MB in 54 us (gate/up
 // 36, down 18); 128 tokens on 107 experts, most on 8 of them, 3.69 GB in 580-600 us,
-// 6.1-6.3 TB/s (gate/up 385-396, down 193-201); on all 128 experts 4.43 GB in 683 us, 6.5 TB/s.
+// 6.1-6.3 TB/s (gate/up 385-396, down 193-201); on all 128 experts 4.43 GB in 683
+// us, 6.5 TB/s.
 #include <type_traits>
 
 #include "device.h"
