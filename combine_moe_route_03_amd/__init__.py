@@ -11,7 +11,8 @@ Entry points mirror include/moe_route.h: ``route``, ``dispatch_index``,
 ``expert_scale``, ``expert_scale_rows``, ``expert_swiglu``, ``combine``,
 ``combine_rows``, ``stats``, and the 8-bit experts and the small layer:
 ``quantize``, ``dispatch_copy_fp8``, ``expert_gemm_fp8``, ``expert_swiglu_fp8``,
-``layer``.
+``layer``; the integer experts and the norm ahead of the router:
+``add_rms_norm``, ``quantize_int8``, ``expert_gemm_int8``, ``expert_swiglu_int8``.
 """
 from __future__ import annotations
 
@@ -26,7 +27,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # build the CPU sanitizer run loads); there is no fallback when it is missing.
 LIB_PATH = os.environ.get("MOE_ROUTE_LIB") or os.path.join(_HERE, "libmoe_route.so")
 
-MOE_F32, MOE_BF16, MOE_F8E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_F8E4M3, MOE_I8 = 0, 1, 2, 3
 _DTYPE_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _CODE_DTYPE = {v: k for k, v in _DTYPE_CODE.items()}
 
@@ -103,6 +104,14 @@ SIGNATURES = {
     "moe_expert_swiglu_fp8_workspace_bytes": ([_shp, _i32], ctypes.c_size_t),
     "moe_expert_swiglu_fp8": ([_shp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                ctypes.c_size_t, _vp], ctypes.c_int),
+    "moe_quantize_int8": ([_vp, _i32, _i32, _i32, _vp, _vp, _vp], ctypes.c_int),
+    "moe_add_rms_norm": ([_i32, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_double, _vp, _vp, _vp,
+                          _vp, _vp], ctypes.c_int),
+    "moe_expert_gemm_int8": ([_i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp,
+                              _i32, _vp, _vp], ctypes.c_int),
+    "moe_expert_swiglu_int8_workspace_bytes": ([_shp, _i32], ctypes.c_size_t),
+    "moe_expert_swiglu_int8": ([_shp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, ctypes.c_size_t, _vp], ctypes.c_int),
     "moe_layer_workspace_bytes": ([_shp, _i32], ctypes.c_size_t),
     "moe_layer": ([_shp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                    ctypes.c_size_t, _vp], ctypes.c_int),
@@ -802,6 +811,159 @@ def expert_swiglu_fp8(send_q: torch.Tensor, send_scale: torch.Tensor,
         _current_stream(dev)), "moe_expert_swiglu_fp8")
     return expert_out
 
+
+# --------------------------------------- integer experts, norm ahead of the router
+
+_Q_CODE = {torch.int8: MOE_I8, _FP8: MOE_F8E4M3}
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                 residual: torch.Tensor | None = None, q_dtype: torch.dtype | None = None,
+                 want_y: bool = True, total: torch.Tensor | None = None,
+                 y: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None):
+    """Root-mean-square norm of t = x + residual (t = x without one), x [..., H] float32
+    or bfloat16: (total, y, q, scale). total is t (None without a residual), y = t /
+    sqrt(mean(t^2) + eps) * weight (None unless want_y), q and scale the unrounded y in
+    8 bits (None without q_dtype or q): int8 with scale [...], or float8_e4m3fn with
+    scale [..., ceil(H/128)]. total and y may be the tensors x and residual."""
+    if x.dtype not in _DTYPE_CODE:
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
+    H = shape[-1]
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    _int32(rows, H)
+    if residual is None and total is not None:
+        raise ValueError("total needs a residual")
+    if residual is not None and total is None:
+        total = _empty(shape, dt, dev)
+    if y is None and want_y:
+        y = _empty(shape, dt, dev)
+    if q is not None:
+        if q_dtype is not None and q_dtype != q.dtype:
+            raise TypeError(f"q must be {q_dtype}, got {q.dtype}")
+        q_dtype = q.dtype
+    if q_dtype is None and scale is not None:
+        raise ValueError("scale needs q or q_dtype")
+    sshape = shape
+    if q_dtype is not None:
+        if q_dtype not in _Q_CODE:
+            raise TypeError(f"q must be int8 or float8_e4m3fn, got {q_dtype}")
+        sshape = shape[:-1] if q_dtype == torch.int8 else (*shape[:-1], _blocks(H))
+        q = _empty(shape, q_dtype, dev) if q is None else q
+        scale = _empty(sshape, torch.float32, dev) if scale is None else scale
+
+    def at(name, t, shape, dtype):
+        return None if t is None else _checked(name, t, shape, dtype, dev)
+
+    _check(lib().moe_add_rms_norm(
+        _DTYPE_CODE[dt], _Q_CODE.get(q_dtype, -1), rows, H, _checked("x", x, shape, dt, dev),
+        at("residual", residual, shape, dt), _checked("weight", weight, (H,), dt, dev), eps,
+        at("total", total, shape, dt), at("y", y, shape, dt), at("q", q, shape, q_dtype),
+        at("scale", scale, sshape, torch.float32), _current_stream(dev)), "moe_add_rms_norm")
+    return total, y, q, scale
+
+
+def quantize_int8(x: torch.Tensor, q: torch.Tensor | None = None,
+                  scale: torch.Tensor | None = None):
+    """Rows of x [..., cols] (float32 or bfloat16) to 8-bit integers: (q int8 of x's
+    shape, scale float32 [...], amax / 127). Weights [E, N, K]: a scale a channel."""
+    if x.dtype not in _DTYPE_CODE:
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    dev, shape = x.device, tuple(x.shape)
+    cols = shape[-1]
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    _int32(rows, cols)
+    q = _empty(shape, torch.int8, dev) if q is None else q
+    scale = _empty(shape[:-1], torch.float32, dev) if scale is None else scale
+    _check(lib().moe_quantize_int8(
+        _checked("x", x, shape, x.dtype, dev), _DTYPE_CODE[x.dtype], rows, cols,
+        _checked("q", q, shape, torch.int8, dev),
+        _checked("scale", scale, shape[:-1], torch.float32, dev), _current_stream(dev)),
+        "moe_quantize_int8")
+    return q, scale
+
+
+def expert_gemm_int8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: torch.Tensor,
+                     expert_counts: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                     row_token: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Each expert's rows times its w [E, N, K] int8, a scale for each row of a (a_scale)
+    and each channel (w_scale [E, N]), into [rows, N] bfloat16 or float32 (out's type, or
+    out_dtype). The rows are those of a [rows, K] int8, or a's rows row_token [rows]."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, K] and w [E, N, K]")
+    dev = a.device
+    a_rows, K = a.shape
+    E, N, _ = w.shape
+    rows = a_rows if row_token is None else row_token.numel()
+    _int32(rows, a_rows, E, N, K)
+    out = _empty((rows, N), out_dtype, dev) if out is None else out
+    if out.dtype not in _DTYPE_CODE:
+        raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
+    f32, i32, i8 = torch.float32, torch.int32, torch.int8
+    _check(lib().moe_expert_gemm_int8(
+        rows, E, N, K, _checked("a", a, (a_rows, K), i8, dev),
+        _checked("a_scale", a_scale, (a_rows,), f32, dev),
+        None if row_token is None else _checked("row_token", row_token, (rows,), i32, dev), a_rows,
+        _checked("expert_offsets", expert_offsets, (E,), i32, dev),
+        _checked("expert_counts", expert_counts, (E,), i32, dev), _checked("w", w, (E, N, K), i8, dev),
+        _checked("w_scale", w_scale, (E, N), f32, dev), _DTYPE_CODE[out.dtype],
+        _checked("out", out, (rows, N), out.dtype, dev), _current_stream(dev)),
+        "moe_expert_gemm_int8")
+    return out
+
+
+def expert_swiglu_int8_workspace_bytes(shape: Shape, I: int) -> int:
+    _int32(I)
+    return int(lib().moe_expert_swiglu_int8_workspace_bytes(ctypes.byref(shape.c()), I))
+
+
+def expert_swiglu_int8(x_q: torch.Tensor, x_scale: torch.Tensor, expert_offsets: torch.Tensor,
+                       expert_counts: torch.Tensor, shape: Shape, w_gate_up: torch.Tensor,
+                       s_gate_up: torch.Tensor, w_down: torch.Tensor, s_down: torch.Tensor,
+                       row_token: torch.Tensor | None = None,
+                       expert_out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """SwiGLU expert FFN on int8 rows and weights (w_gate_up [E, 2I, H], w_down [E, H, I]
+    int8, scales [E, 2I] and [E, H]) into bfloat16 [T*k, H]. x_q [T*k, H] in expert order,
+    or, with row_token [T*k] (dispatch_index's), [T, H] in token order. shape.dtype is
+    the output's: bfloat16."""
+    dev = x_q.device
+    E, H, rows = shape.E, shape.H, shape.T * shape.k
+    I = w_down.shape[-1]
+    _int32(I)
+    a_rows = rows if row_token is None else shape.T
+    f32, i32, i8 = torch.float32, torch.int32, torch.int8
+    expert_out = _empty((rows, H), torch.bfloat16, dev) if expert_out is None else expert_out
+    sh = ctypes.byref(shape.c())
+    if workspace is None:
+        workspace = _workspace(None, int(lib().moe_expert_swiglu_int8_workspace_bytes(sh, I)), dev)
+    _check(lib().moe_expert_swiglu_int8(
+        sh, I, _checked("x_q", x_q, (a_rows, H), i8, dev),
+        _checked("x_scale", x_scale, (a_rows,), f32, dev),
+        None if row_token is None else _checked("row_token", row_token, (rows,), i32, dev),
+        _checked("expert_offsets", expert_offsets, (E,), i32, dev),
+        _checked("expert_counts", expert_counts, (E,), i32, dev),
+        _checked("w_gate_up", w_gate_up, (E, 2 * I, H), i8, dev),
+        _checked("s_gate_up", s_gate_up, (E, 2 * I), f32, dev),
+        _checked("w_down", w_down, (E, H, I), i8, dev),
+        _checked("s_down", s_down, (E, H), f32, dev),
+        _checked("expert_out", expert_out, (rows, H), torch.bfloat16, dev),
+        _checked("workspace", workspace, tuple(workspace.shape), torch.uint8, dev), workspace.numel(),
+        _current_stream(dev)), "moe_expert_swiglu_int8")
+    return expert_out
+
+
+# ------------------------------------------------------------------ small layer
 
 def layer_workspace_bytes(shape: Shape, I: int) -> int:
     _int32(I)

@@ -16,7 +16,8 @@ LIB = os.path.join(PKG, "libmoe_route.so")
 SOURCES = ["abi.hip", "route.hip", "dispatch.hip", "combine.hip", "expert.hip", "ffn.hip",
            "stats.hip", "alpha.hip", "exchange.hip", "waves.hip", "dispatch_small.hip",
            "combine_waves.hip", "quant.hip", "gemm_fp8.hip",
-           "gemm_fp8_stream.hip", "layer.hip"]
+           "gemm_fp8_stream.hip", "layer.hip", "norm.hip", "gemm_int8.hip",
+           "gemm_int8_stream.hip"]
 
 # -packed-fp32-ops off: plain fp32 VALU code only (no v_pk_*_f32 forms).
 HIPFLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -764,6 +764,33 @@ int check_gemm_fp8_sizes(int64_t rows, int64_t E, int64_t N, int64_t K) {
   return MOE_OK;
 }
 
+// Rows of the norm and of the integer quantisation: 16-byte vectors counted in 32 bits,
+// a row in one block, grids of less than 2^32 threads.
+int check_row_sizes(int32_t dtype, int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1) return MOE_ERR_ARG;
+  if (cols % 16 != 0) return MOE_ERR_ALIGN;
+  if (cols > moe::kMaxRow) return MOE_ERR_ARG;
+  if (rows * (dtype == MOE_BF16 ? 16 : 32) * ceil_div(cols, 128) >= kIndexLimit) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+// As check_gemm_fp8_sizes; sums of K products of two magnitudes up to 128 fit 32 bits.
+int check_gemm_int8_sizes(int64_t rows, int64_t E, int64_t N, int64_t K, const int32_t* row_token,
+                          int64_t a_rows) {
+  if (rows < 0 || rows >= kIndexLimit || E < 1 || E > 1024 || N < 16 || N % 16 != 0 || K < 16 ||
+      K % 16 != 0 || K >= (int64_t(1) << 17))
+    return MOE_ERR_ARG;
+  if (N * K >= (int64_t(1) << 31) || 512 * N >= (int64_t(1) << 30)) return MOE_ERR_ARG;
+  if (E * N * K >= (int64_t(1) << 40)) return MOE_ERR_ARG;
+  if (a_rows < 0 || (row_token ? a_rows * K >= (int64_t(1) << 31) : rows > 0 && a_rows != rows))
+    return MOE_ERR_ARG;
+  const int64_t mtiles = rows / moe::kStreamRows + (rows < E ? rows : E);
+  if (mtiles * ceil_div(N, 128) >= (int64_t(1) << 30)) return MOE_ERR_ARG;
+  if (mtiles * ceil_div(N, 32) >= (int64_t(1) << 32) / moe::kStreamThreads - 64)
+    return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
 int check_layer_shape(const moe_shape* sh, int32_t I) {
   const int st = check_shape(sh);
   if (st != MOE_OK) return st;
@@ -867,6 +894,95 @@ int moe_expert_swiglu_fp8(const moe_shape* shape, int32_t I, const void* send_q,
       send_q, send_scale, rows, shape->H, I, shape->E, expert_offsets, expert_counts, w_gate_up,
       s_gate_up, w_down, s_down, ws, reinterpret_cast<float*>(ws + round256(rows * I)), expert_out,
       as_stream(stream)));
+}
+
+int moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32_t cols, void* q,
+                      float* scale, moe_stream_t stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  const int st = check_row_sizes(dtype, rows, cols);
+  if (st != MOE_OK) return st;
+  if (rows > 0 && (!x || !q || !scale)) return MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_ALIGN;
+  return status_of(moe::launch_quantize_int8(x, dtype, rows, cols, q, scale, as_stream(stream)));
+}
+
+int moe_add_rms_norm(int32_t dtype, int32_t q_dtype, int32_t T, int32_t H, const void* x,
+                     const void* residual, const void* weight, double eps, void* total, void* y,
+                     void* q, float* scale, moe_stream_t stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (q && q_dtype != MOE_I8 && q_dtype != MOE_F8E4M3) return MOE_ERR_UNSUPPORTED;
+  const int st = check_row_sizes(dtype, T, H);
+  if (st != MOE_OK) return st;
+  if (!(eps >= 0.0) || std::isinf(eps)) return MOE_ERR_ARG;
+  if (!weight || (T > 0 && !x) || (q && !scale)) return MOE_ERR_ARG;
+  if (T > 0 && (!residual != !total || (!total && !y && !q))) return MOE_ERR_ARG;
+  if (total && total == y) return MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(total, 16) ||
+      !aligned(y, 16) || !aligned(q, 16) || !aligned(scale, 4))
+    return MOE_ERR_ALIGN;
+  return status_of(moe::launch_add_rms_norm(dtype, q_dtype, T, H, x, residual, weight, eps, total,
+                                            y, q, scale, as_stream(stream)));
+}
+
+int moe_expert_gemm_int8(int32_t rows, int32_t E, int32_t N, int32_t K, const void* a,
+                         const float* a_scale, const int32_t* row_token, int32_t a_rows,
+                         const int32_t* expert_offsets, const int32_t* expert_counts,
+                         const void* w, const float* w_scale, int32_t out_dtype, void* out,
+                         moe_stream_t stream) {
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  const int st = check_gemm_int8_sizes(rows, E, N, K, row_token, a_rows);
+  if (st != MOE_OK) return st;
+  if (!expert_offsets || !expert_counts || !w || !w_scale) return MOE_ERR_ARG;
+  if (rows > 0 && (!out || (a_rows > 0 && (!a || !a_scale)))) return MOE_ERR_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(w_scale, 16) || !aligned(out, 16) ||
+      !aligned(a_scale, 4) || !aligned(row_token, 4) || !aligned(expert_offsets, 4) ||
+      !aligned(expert_counts, 4))
+    return MOE_ERR_ALIGN;
+  return status_of(moe::launch_gemm_int8({a, a_scale, row_token, a_rows}, rows, E, expert_offsets,
+                                         expert_counts, w, w_scale, N, K, out_dtype, out,
+                                         as_stream(stream)));
+}
+
+size_t moe_expert_swiglu_int8_workspace_bytes(const moe_shape* shape, int32_t I) {
+  if (check_shape(shape) != MOE_OK || I < 16 || I % 16 != 0 || I > moe::kMaxRow) return 0;
+  const int64_t rows = int64_t(shape->T) * shape->k;
+  return size_t(round256(rows * I * 4) + round256(rows * I) + round256(rows * 4));
+}
+
+int moe_expert_swiglu_int8(const moe_shape* shape, int32_t I, const void* x_q,
+                           const float* x_scale, const int32_t* row_token,
+                           const int32_t* expert_offsets, const int32_t* expert_counts,
+                           const void* w_gate_up, const float* s_gate_up, const void* w_down,
+                           const float* s_down, void* expert_out, void* workspace,
+                           size_t workspace_bytes_given, moe_stream_t stream) {
+  int st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (shape->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (I < 16 || I % 16 != 0 || I > moe::kMaxRow || shape->H % 16 != 0) return MOE_ERR_ARG;
+  const int64_t rows = int64_t(shape->T) * shape->k;
+  const int64_t a_rows = row_token ? shape->T : rows;
+  if (rows * ceil_div(I, 128) >= (int64_t(1) << 26)) return MOE_ERR_ARG;
+  if ((st = check_gemm_int8_sizes(rows, shape->E, int64_t(2) * I, shape->H, row_token, a_rows)) !=
+      MOE_OK)
+    return st;
+  if ((st = check_gemm_int8_sizes(rows, shape->E, shape->H, I, nullptr, rows)) != MOE_OK) return st;
+  if (!expert_offsets || !expert_counts || !w_gate_up || !s_gate_up || !w_down || !s_down ||
+      !workspace)
+    return MOE_ERR_ARG;
+  if (rows > 0 && (!x_q || !x_scale || !expert_out)) return MOE_ERR_ARG;
+  if (!aligned(x_q, 16) || !aligned(expert_out, 16) || !aligned(w_gate_up, 16) ||
+      !aligned(w_down, 16) || !aligned(s_gate_up, 16) || !aligned(s_down, 16) ||
+      !aligned(workspace, 16) || !aligned(x_scale, 4) || !aligned(row_token, 4) ||
+      !aligned(expert_offsets, 4) || !aligned(expert_counts, 4))
+    return MOE_ERR_ALIGN;
+  if (workspace_bytes_given < moe_expert_swiglu_int8_workspace_bytes(shape, I))
+    return MOE_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  char* hq = ws + round256(rows * I * 4);
+  return status_of(moe::launch_expert_swiglu_int8(
+      {x_q, x_scale, row_token, a_rows}, rows, shape->H, I, shape->E, expert_offsets,
+      expert_counts, w_gate_up, s_gate_up, w_down, s_down, reinterpret_cast<float*>(ws), hq,
+      reinterpret_cast<float*>(hq + round256(rows * I)), expert_out, as_stream(stream)));
 }
 
 size_t moe_layer_workspace_bytes(const moe_shape* shape, int32_t I) {

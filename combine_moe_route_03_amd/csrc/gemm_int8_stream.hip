@@ -1,0 +1,250 @@
+// gemm_int8_stream.hip -- grouped products of 8-bit integer rows with 8-bit integer
+// expert weights for few rows an expert, where the weights' HBM bytes bound them:
+// each live expert's weights are streamed once from memory through registers
+// (stream.h), a block taking up to 32 rows of an expert.
+//
+//   out[m][n] = sa[m] sw[n] sum_j a[m][j] w[n][j],  the sum exact in 32 bits
+//   gate/up:  h = SiLU(g) u in fp32, g and u as above
+//
+// A wave computes 32 weight rows by up to 32 tokens, K steps of 128 bytes. With one
+// scale a row and a column the sums need no step of their own: the matrix instruction
+// adds them up through the whole of K.
+#include <type_traits>
+
+#include "device.h"
+#include "ffn_device.h"
+#include "gemm_int8.h"
+#include "launch.h"
+#include "stream.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRows = kStreamRows;  // rows of a tile
+constexpr int kWaves = kStreamThreads / kWave;
+constexpr int kStageBytes = 4096 + kRows * 128;  // a wave's LDS: a step's weights and tokens
+
+// Steps in flight: what fits 128 registers (four waves a SIMD).
+template <int NB>
+constexpr int kRing = NB == 4 ? 2 : 3;
+
+// acc[f][t] += products of weight fragment f (16 rows) with tokens 16 t .. 16 t + 15
+// over the K steps s0 .. s0 + n - 1, beginning with step s0 + rot. woff: byte offsets in
+// wb of the lane's four weight rows (two a fragment) at its chunk, wrow their LDS rows in
+// the fragment; xoff[b]: in xb of its token of group b at its chunk (kOutside: none).
+// last, keep: the step that holds the end of a row, and whether the lane's chunk of it is
+// in the row; past it the tokens are zeros, so it does not matter what the weights are.
+// kShared: other blocks read these weights.
+template <int NB, bool kShared>
+__device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
+                                          const uint32_t (&woff)[4], const int (&wrow)[2],
+                                          const Buffer& xb, const uint32_t (&xoff)[NB], int s0,
+                                          int n, int rot, int last, bool keep,
+                                          i32x4 (&acc)[2][(NB + 1) / 2]) {
+  constexpr int NTL = (NB + 1) / 2, D = kRing<NB>;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int lr = lane >> 3, lc = lane & 7, i = lane & 15, g = lane >> 4;
+  v4u w[D][4], x[D][NB];
+  auto load = [&](int u, int q) __attribute__((always_inline)) {
+    const bool in = q < n;
+    const uint32_t s = in ? (uint32_t)(s0 + (q + rot >= n ? q + rot - n : q + rot)) : 0;
+    const bool cut = (int)s == last && !keep;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      w[u][r] = kShared ? load16(wb.at(in), woff[r], s * 128)
+                        : load16_stream(wb.at(in), woff[r], s * 128);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) x[u][b] = load16(xb.at(in), cut ? kOutside : xoff[b], s * 128);
+  };
+  uint8_t* xs = stage + 4096;
+  auto frag = [&](const uint8_t* base, int r, int c) __attribute__((always_inline)) -> i32x4 {
+    return *reinterpret_cast<const i32x4*>(base + tile_at(r, c));
+  };
+  auto compute = [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<v4u*>(stage + 2048 * (r >> 1) + tile_at(wrow[r & 1], lc)) = w[u][r];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) *reinterpret_cast<v4u*>(xs + tile_at(8 * b + lr, lc)) = x[u][b];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // halves of the 128 bytes
+      const i32x4 a[2] = {frag(stage, i, g + 4 * h), frag(stage + 2048, i, g + 4 * h)};
+#pragma unroll
+      for (int t = 0; t < NTL; ++t) {
+        // with one group of 8 tokens its rows twice (columns 8-15 unused)
+        const i32x4 tok = frag(xs, NB == 1 ? i & 7 : 16 * t + i, g + 4 * h);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) acc[f][t] = mfma_int8(a[f], tok, acc[f][t]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+#pragma unroll
+  for (int u = 0; u < D; ++u) load(u, u);
+  for (int q = 0; q < n; q += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      compute(u);  // past the last step: zeros
+      load(u, q + u + D);
+    }
+  }
+}
+
+// A block: one tile of up to kRows rows; its 8 waves are 8 / WK groups of 32 weight rows,
+// each group's WK waves taking a share of K whose sums meet in LDS. Plain: 32 output
+// columns a group. Gate/up: 16 columns a group (their gate and up rows interleaved in a
+// fragment so that a lane's four results are g, g, u, u of two neighbouring columns), C
+// = h in fp32. N: rows of one expert's B (2 I for gate/up). tokens: rows of A that idx
+// may name, or null and A's rows lie in expert order.
+template <bool kGateUp, int WK, bool kF32Out>
+__global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
+    const uint8_t* __restrict__ A, const float* __restrict__ Asc, const int32_t* __restrict__ idx,
+    uint32_t tokens, const int32_t* __restrict__ offs, const int32_t* __restrict__ cnts, int E,
+    int64_t rows_total, const uint8_t* __restrict__ B, const float* __restrict__ Bsc, int N, int K,
+    void* __restrict__ C, int ntiles) {
+  constexpr int kGroups = kWaves / WK;
+  constexpr int kGroupCols = kGateUp ? 16 : 32;
+  constexpr int kNO = kGroups * kGroupCols;  // output columns of a tile
+  __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][kStageBytes];
+  __shared__ int info[4];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const Tile tile = find_tile<kRows>(offs, cnts, E, rows_total, ntiles, info);
+  if (tile.e < 0) return;  // uniform over the block
+  const int e = tile.e, row0 = tile.row0, rows = tile.rows;
+  const int i = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
+  const int KB = (K + 127) / 128, I = N / 2;
+  const int group = wid / WK, part = wid % WK;
+  const Buffer wb = {B + (int64_t)e * N * K, (uint32_t)N * (uint32_t)K};
+  const Buffer xb = {idx ? A : A + (int64_t)row0 * K,
+                     (idx ? tokens : (uint32_t)rows) * (uint32_t)K};
+  const int n0 = tile.ntile * kNO + group * kGroupCols;  // the group's first column
+  uint32_t woff[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    // gate/up: gate and up rows of 8 columns a fragment; plain: 8 rows each (those
+    // past the last one, in the last tile, do not exist)
+    const int c = kGateUp ? n0 + 8 * (r >> 1) + lr : n0 + 8 * r + lr;
+    const int n = kGateUp ? (r & 1 ? I : 0) + c : c;
+    woff[r] = c < (kGateUp ? I : N) ? (uint32_t)n * (uint32_t)K + 16 * lc : kOutside;
+  }
+  const int wrow[2] = {kGateUp ? 4 * (lr >> 1) + (lr & 1) : lr,
+                       kGateUp ? 4 * (lr >> 1) + (lr & 1) + 2 : 8 + lr};
+  // the row of A behind row m of the tile (tokens where there is none)
+  const auto source = [&](int m) -> uint32_t {
+    if (m >= rows) return tokens;
+    return idx ? (uint32_t)idx[row0 + m] : (uint32_t)(row0 + m);
+  };
+
+  auto pass = [&](auto nb_, auto shared) __attribute__((always_inline)) {
+    constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
+    uint32_t xoff[NB];
+    i32x4 acc[2][NTL];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t m = 8 * b + lr, r = idx ? source(m) : m;
+      xoff[b] = (int)m < rows && (!idx || r < tokens) ? r * (uint32_t)K + 16 * lc : kOutside;
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int t = 0; t < NTL; ++t) acc[f][t] = i32x4{0, 0, 0, 0};
+    const int s0 = KB * part / WK, n = KB * (part + 1) / WK - s0;
+    if (n > 0)  // uniform over the wave
+      dot_steps<NB, decltype(shared)::value>(stage[wid], wb, woff, wrow, xb, xoff, s0, n,
+                                             (tile.ntile + row0) * 5 % n, KB - 1,
+                                             16 * lc < K - 128 * (KB - 1), acc);
+    // lane l's results of fragments f and t: columns n0 + 16 f (8 f) + ..., token 16 t + i
+    const auto emit = [&](int f, int t, i32x4 v) __attribute__((always_inline)) {
+      const int m = 16 * t + i;
+      if (m >= rows || (NB == 1 && i >= 8)) return;
+      const uint32_t r = source(m);
+      const float sa = r < tokens ? Asc[r] : 0.f;
+      const float* ws = Bsc + (int64_t)e * N;
+      if constexpr (kGateUp) {
+        const int n = n0 + 8 * f + 2 * g;
+        if (n >= I) return;
+        const float2 sg = *reinterpret_cast<const float2*>(ws + n);
+        const float2 su = *reinterpret_cast<const float2*>(ws + I + n);
+        float2 h;
+        h.x = silu(scaled(v[0], sa, sg.x)) * scaled(v[2], sa, su.x);
+        h.y = silu(scaled(v[1], sa, sg.y)) * scaled(v[3], sa, su.y);
+        *reinterpret_cast<float2*>(static_cast<float*>(C) + (int64_t)(row0 + m) * I + n) = h;
+      } else {
+        const int n = n0 + 16 * f + 4 * g;
+        if (n >= N) return;
+        const float4 sw = *reinterpret_cast<const float4*>(ws + n);
+        const float o[4] = {scaled(v[0], sa, sw.x), scaled(v[1], sa, sw.y), scaled(v[2], sa, sw.z),
+                            scaled(v[3], sa, sw.w)};
+        const int64_t at = (int64_t)(row0 + m) * N + n;
+        if constexpr (kF32Out)
+          *reinterpret_cast<float4*>(static_cast<float*>(C) + at) = make_float4(o[0], o[1], o[2], o[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(C) + at) =
+              make_uint2(bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3]));
+      }
+    };
+    if constexpr (WK == 1) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) emit(f, t, acc[f][t]);
+    } else {
+      // every wave's sums behind its stage; the group's waves share the fragments
+      constexpr int kFrags = 2 * NTL;
+      i32x4* own = reinterpret_cast<i32x4*>(stage[wid]);
+      static_assert(kFrags * kWave * 16 <= kStageBytes, "sums fit the stage");
+#pragma unroll
+      for (int j = 0; j < kFrags; ++j) own[j * kWave + lane] = acc[j / NTL][j % NTL];
+      __syncthreads();
+      for (int j = part; j < kFrags; j += WK) {
+        i32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WK; ++w)
+          v += reinterpret_cast<const i32x4*>(stage[group * WK + w])[j * kWave + lane];
+        emit(j / NTL, j % NTL, v);
+      }
+    }
+  };
+  // the expert's other tiles read the same weights
+  if (cnts[e] > kRows) pass(std::integral_constant<int, 4>{}, std::true_type{});
+  else if (rows <= 8) pass(std::integral_constant<int, 1>{}, std::false_type{});
+  else if (rows <= 16) pass(std::integral_constant<int, 2>{}, std::false_type{});
+  else pass(std::integral_constant<int, 4>{}, std::false_type{});
+}
+
+template <bool kGateUp, int WK, bool kF32Out>
+hipError_t run(const Int8Rows& a, int64_t rows, int E, const int32_t* offs, const int32_t* cnts,
+               const void* w, const float* wsc, int N, int K, void* c, hipStream_t s) {
+  const int cols = kGateUp ? N / 2 : N;
+  constexpr int kNO = kWaves / WK * (kGateUp ? 16 : 32);
+  const int ntiles = (cols + kNO - 1) / kNO;
+  const int64_t mt = rows / kRows + (rows < E ? rows : E);
+  const int64_t runs = (mt * ntiles + kGroupM * kXCD - 1) / (kGroupM * kXCD);
+  return launch(gemm_int8_stream_kernel<kGateUp, WK, kF32Out>,
+                dim3((unsigned)(runs * kGroupM * kXCD)), dim3(kWave * kWaves), 0, s,
+                static_cast<const uint8_t*>(a.q), a.scale, a.index, (uint32_t)a.rows, offs, cnts, E,
+                rows, static_cast<const uint8_t*>(w), wsc, N, K, c, ntiles);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_int8_stream(bool gate_up, bool f32_out, const Int8Rows& a, int64_t rows,
+                                   int E, const int32_t* offs, const int32_t* cnts, const void* w,
+                                   const float* wsc, int N, int K, void* c, hipStream_t s) {
+  const auto with = [&](auto wk) {
+    constexpr int WK = decltype(wk)::value;
+    if (gate_up) return run<true, WK, true>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
+    return f32_out ? run<false, WK, true>(a, rows, E, offs, cnts, w, wsc, N, K, c, s)
+                   : run<false, WK, false>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
+  };
+  switch (gemm_int8_splits(rows, E, N, K)) {
+    case 1: return with(std::integral_constant<int, 1>{});
+    case 2: return with(std::integral_constant<int, 2>{});
+    case 4: return with(std::integral_constant<int, 4>{});
+    default: return with(std::integral_constant<int, 8>{});
+  }
+}
+
+}  // namespace moe

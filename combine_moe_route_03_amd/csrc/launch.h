@@ -260,6 +260,50 @@ hipError_t launch_expert_swiglu_fp8(const void* send, const float* ssc, int64_t 
                                     const void* w_gate_up, const float* gsc, const void* w_down,
                                     const float* dsc, void* hq, float* hs, void* out,
                                     hipStream_t s);
+// Root-mean-square norm of t = x + residual (null: x) [T][H] into y (may be null), with
+// 8-bit rows into q (null: none) in the format of q_dtype (MOE_I8: a scale a row;
+// MOE_F8E4M3: a scale a 128 columns). H % 16 == 0, H <= kMaxRow.
+constexpr int kMaxRow = 65536;
+hipError_t launch_add_rms_norm(int dtype, int q_dtype, int T, int H, const void* x,
+                               const void* residual, const void* weight, double eps, void* total,
+                               void* y, void* q, float* scale, hipStream_t s);
+// Rows [rows][cols] to int8 with a scale each; cols % 16 == 0, cols <= kMaxRow.
+hipError_t launch_quantize_int8(const void* x, int dtype, int64_t rows, int cols, void* q,
+                                float* scale, hipStream_t s);
+// Rows of an int8 product: q [rows][K] with a scale each, in expert order (index null,
+// rows as many as the product has), or picked by index[row of the product].
+struct Int8Rows {
+  const void* q;
+  const float* scale;
+  const int32_t* index;
+  int64_t rows;
+};
+// Grouped product of int8 rows and weights [E][N][K] with a scale each into bf16 or fp32
+// rows of N; K % 16 == 0, N % 16 == 0.
+hipError_t launch_gemm_int8(const Int8Rows& a, int64_t rows, int E, const int32_t* offs,
+                            const int32_t* cnts, const void* w, const float* wsc, int N, int K,
+                            int out_dtype, void* out, hipStream_t s);
+// The waves that share one group of weight rows in the streamed kernel, each a part of K:
+// 1 where that already makes two blocks a compute unit (a tile: kStreamRows rows by
+// kStreamCols / parts), more where it does not.
+inline int gemm_int8_splits(int64_t rows, int64_t E, int64_t N, int64_t K) {
+  const int64_t mt = rows / kStreamRows + (rows < E ? rows : E);
+  int parts = 1;
+  while (parts < 8 && K > 256 * parts && mt * ((N * parts + kStreamCols - 1) / kStreamCols) < 512)
+    parts *= 2;
+  return parts;
+}
+// gate_up: N = 2 I, c = h in fp32 [rows][I].
+hipError_t launch_gemm_int8_stream(bool gate_up, bool f32_out, const Int8Rows& a, int64_t rows,
+                                   int E, const int32_t* offs, const int32_t* cnts, const void* w,
+                                   const float* wsc, int N, int K, void* c, hipStream_t s);
+// The SwiGLU FFN on int8 rows: gate/up product with h = SiLU(g) u into h [rows][I] fp32,
+// its rows to hq and hs, the down product.
+hipError_t launch_expert_swiglu_int8(const Int8Rows& a, int64_t rows, int H, int I, int E,
+                                     const int32_t* offs, const int32_t* cnts,
+                                     const void* w_gate_up, const float* gsc, const void* w_down,
+                                     const float* dsc, float* h, void* hq, float* hs, void* out,
+                                     hipStream_t s);
 // The MoE layer of a few tokens (T <= kLayerMaxT, T*k <= 1024): routing, gate/up
 // into h [T*k][I] bf16, down and combine into y. plan: layer_plan_ints int32.
 constexpr int kLayerMaxT = 128;

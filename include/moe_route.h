@@ -66,7 +66,8 @@ typedef enum {
 typedef enum {
   MOE_F32 = 0,
   MOE_BF16 = 1,
-  MOE_F8E4M3 = 2 /* weights of moe_layer only; a shape's dtype is one of the others */
+  MOE_F8E4M3 = 2, /* 8-bit formats (weights of moe_layer, rows of moe_add_rms_norm); a */
+  MOE_I8 = 3      /* shape's dtype is one of the others */
 } moe_dtype;
 
 /* Problem shape shared by the dispatch, expert and combine calls. */
@@ -393,6 +394,88 @@ int moe_expert_swiglu_fp8(const moe_shape* shape, int32_t I, const void* send_q,
                           const float* s_gate_up, const void* w_down, const float* s_down,
                           void* expert_out, void* workspace, size_t workspace_bytes,
                           moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Integer experts, and the norm ahead of the router. Values are 8-bit integers with one
+ * fp32 scale for each row (tokens: [rows]; weights: one for each output channel, [E][N]);
+ * a value stands for q * scale. */
+
+/* Rows of x [rows][cols] (dtype MOE_F32 or MOE_BF16) to q int8 [rows][cols] and scale
+ * [rows]: amax = the largest finite magnitude of the row, scale = amax / 127 rounded to
+ * fp32 (at least 2^-126; 1 when amax is 0), q = the integer nearest to x / scale (the
+ * exact quotient; ties to even). Infinities saturate to +-127; a row with a NaN has scale
+ * NaN and q 0. Tokens are rows; so are the channels of weights [E][N][K], with rows = E * N.
+ * cols % 16 == 0, cols <= 65536; rows * ceil(cols/128) < 2^27 for bf16, 2^26 for fp32;
+ * x and q 16-byte aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also
+ * cols % 16), MOE_ERR_UNSUPPORTED (dtype), MOE_ERR_DEVICE. */
+int moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32_t cols, void* q,
+                      float* scale, moe_stream_t stream);
+
+/* Root-mean-square norm with the residual's addition, and its rows in 8 bits:
+ *   t = round_dtype(x + residual)   (residual NULL: t = x)
+ *   y = t * weight / sqrt( sum_j t_j^2 / H + eps )
+ * for each of T rows of H. total (with a residual): t; y (or NULL): rounded once to dtype;
+ * q (or NULL) and scale: the unrounded y, in the format of q_dtype:
+ *   MOE_I8      int8, scale [T], as moe_quantize_int8 (scale at most the largest fp32)
+ *   MOE_F8E4M3  e4m3, scale [T][ceil(H/128)], as moe_quantize with block_rows 1
+ * Sums, the norm and y are held in 64 bits. What the formula makes of infinities and NaN
+ * holds: an infinite t gives y NaN there and 0 elsewhere; eps 0 and a row of zeros NaN.
+ * x, residual, total, y [T][H] and weight [H] all of `dtype` (MOE_F32 or MOE_BF16). total
+ * and y may each be the buffer of x or of the residual (not both the same one); no other
+ * buffers may overlap. 0 <= eps < infinity; H % 16 == 0, H <= 65536, T * ceil(H/128) <
+ * 2^27 for bf16, 2^26 for fp32; scale 4-byte, all others 16-byte aligned. One launch.
+ * Errors: MOE_ERR_ARG (also a residual without total or total without one, or none of
+ * total, y and q), MOE_ERR_ALIGN (also H % 16), MOE_ERR_UNSUPPORTED (dtype, or q_dtype with a q),
+ * MOE_ERR_DEVICE. */
+int moe_add_rms_norm(int32_t dtype, int32_t q_dtype, int32_t T, int32_t H, const void* x,
+                     const void* residual, const void* weight, double eps, void* total, void* y,
+                     void* q, float* scale, moe_stream_t stream);
+
+/* Grouped product of int8 rows with int8 expert weights, on MFMA:
+ *   out[n][c] = round( S a_scale[r] w_scale[e][c] ),  S = sum_j a[r][j] w[e][c][j]
+ * for every row n in [expert_offsets[e], + expert_counts[e]); other rows are untouched.
+ * r = n, or row_token[n] where row_token is given: the rows are then picked from a_rows
+ * tokens and need no dispatch copy (an index outside [0, a_rows) gives a row of zeros). S is
+ * exact; it and its products with the two scales, in that order, are rounded to fp32,
+ * the last one once more to out_dtype (MOE_BF16 or MOE_F32). A dense product is E = 1 with offsets {0}
+ * and counts {rows}. Buckets may lie in any order and do not overlap; one that does not lie
+ * in [0, rows) gives no output.
+ * a [a_rows][K] int8 (a_rows == rows without row_token), a_scale [a_rows], w [E][N][K] int8,
+ * w_scale [E][N], out [rows][N]. K % 16 == 0, K < 2^17, N % 16 == 0, 1 <= E <= 1024,
+ * N*K < 2^31, 512*N < 2^30, E*N*K < 2^40, with row_token a_rows*K < 2^31, fewer than 2^30
+ * tiles of 32 rows (+ min(rows, E)) by 128 columns, with at most 28 * E rows fewer than 2^23 - 64
+ * by 32; a, w, w_scale, out 16-byte aligned.
+ * One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (out_dtype),
+ * MOE_ERR_DEVICE. */
+int moe_expert_gemm_int8(int32_t rows, int32_t E, int32_t N, int32_t K, const void* a,
+                         const float* a_scale, const int32_t* row_token, int32_t a_rows,
+                         const int32_t* expert_offsets, const int32_t* expert_counts,
+                         const void* w, const float* w_scale, int32_t out_dtype, void* out,
+                         moe_stream_t stream);
+
+/* Bytes of device workspace moe_expert_swiglu_int8 needs (the inner rows in fp32 and in
+ * int8, and their scales); 0 for an invalid shape or I. Host-only, pure. */
+size_t moe_expert_swiglu_int8_workspace_bytes(const moe_shape* shape, int32_t I);
+
+/* moe_expert_swiglu on int8 rows and weights: g and u as moe_expert_gemm_int8 (fp32),
+ * h = g / (1 + exp(-g)) * u in fp32, its rows quantised as moe_quantize_int8 does, into the
+ * workspace, expert_out the moe_expert_gemm_int8 product of those with w_down.
+ * shape->dtype is the type of expert_out: MOE_BF16 only. row_token NULL: x_q int8 [T*k][H]
+ * and x_scale [T*k] in expert order. Else x_q [T][H] and x_scale [T] in token order and
+ * row_token [T*k] as moe_dispatch_index writes it: no dispatch copy is needed. w_gate_up
+ * [E][2I][H] (rows 0..I-1 gate, I..2I-1 up), s_gate_up [E][2I], w_down [E][H][I], s_down
+ * [E][H], expert_out [T*k][H] bf16. H % 16 == 0, I % 16 == 0, I <= 65536,
+ * T * k * ceil(I/128) < 2^26 and the limits of moe_expert_gemm_int8 for both products. workspace:
+ * moe_expert_swiglu_int8_workspace_bytes(shape, I) bytes, 16-byte aligned, clobbered; calls
+ * that overlap need one each. Three launches.
+ * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_UNSUPPORTED,
+ *         MOE_ERR_DEVICE. */
+int moe_expert_swiglu_int8(const moe_shape* shape, int32_t I, const void* x_q,
+                           const float* x_scale, const int32_t* row_token,
+                           const int32_t* expert_offsets, const int32_t* expert_counts,
+                           const void* w_gate_up, const float* s_gate_up, const void* w_down,
+                           const float* s_down, void* expert_out, void* workspace,
+                           size_t workspace_bytes, moe_stream_t stream);
 
 /* Bytes of device workspace moe_layer needs; 0 for an invalid shape or I.
  * Host-only, pure. */
