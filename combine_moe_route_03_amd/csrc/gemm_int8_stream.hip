@@ -117,8 +117,9 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
   const int KB = (K + 127) / 128, I = N / 2;
   const int group = wid / WK, part = wid % WK;
   const Buffer wb = {B + (int64_t)e * N * K, (uint32_t)N * (uint32_t)K};
+  // (never shorter than a step's offset: without tokens every lane's row is outside)
   const Buffer xb = {idx ? A : A + (int64_t)row0 * K,
-                     (idx ? tokens : (uint32_t)rows) * (uint32_t)K};
+                     (idx ? (tokens ? tokens : 1) : (uint32_t)rows) * (uint32_t)K};
   const int n0 = tile.ntile * kNO + group * kGroupCols;  // the group's first column
   uint32_t woff[4];
 #pragma unroll
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
     const int s0 = KB * part / WK, n = KB * (part + 1) / WK - s0;
     if (n > 0)  // uniform over the wave
       dot_steps<NB, decltype(shared)::value>(stage[wid], wb, woff, wrow, xb, xoff, s0, n,
-                                             (tile.ntile + row0) * 5 % n, KB - 1,
+                                             (int)((uint32_t)(tile.ntile + row0) * 5 % (uint32_t)n), KB - 1,
                                              16 * lc < K - 128 * (KB - 1), acc);
     // lane l's results of fragments f and t: columns n0 + 16 f (8 f) + ..., token 16 t + i
     const auto emit = [&](int f, int t, i32x4 v) __attribute__((always_inline)) {

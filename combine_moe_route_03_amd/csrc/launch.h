@@ -283,6 +283,11 @@ struct Int8Rows {
 hipError_t launch_gemm_int8(const Int8Rows& a, int64_t rows, int E, const int32_t* offs,
                             const int32_t* cnts, const void* w, const float* wsc, int N, int K,
                             int out_dtype, void* out, hipStream_t s);
+// Whether that product (or the gate/up product) streams the weights in 32-row tiles. One K
+// step is too short for the tiled kernel's stream of loads.
+inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t K) {
+  return K <= 128 || rows <= kFewRows * E;
+}
 // The waves that share one group of weight rows in the streamed kernel, each a part of K:
 // 1 where that already makes two blocks a compute unit (a tile: kStreamRows rows by
 // kStreamCols / parts), more where it does not.

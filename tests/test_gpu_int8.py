@@ -72,12 +72,13 @@ def test_gemm_rows_by_index(N, K, counts):
           scales(E, N, seed=9), index=index)
 
 
-def test_gemm_no_tokens():
+@pytest.mark.parametrize("rows,K", [(1, 64), (20, 400), (40, 64), (40, 400), (300, 1040)])
+def test_gemm_no_tokens(rows, K):
     """Rows by index into no tokens are rows of zeros."""
-    index = torch.zeros(40, **I32)
-    a, sa = torch.empty(0, 64, device=DEV, dtype=torch.int8), torch.empty(0, device=DEV)
-    out = moe.expert_gemm_int8(a, sa, torch.tensor([0], **I32), torch.tensor([40], **I32),
-                               ints(1, 32, 64, seed=1), scales(1, 32, seed=2), row_token=index)
+    index = torch.zeros(rows, **I32)
+    a, sa = torch.empty(0, K, device=DEV, dtype=torch.int8), torch.empty(0, device=DEV)
+    out = moe.expert_gemm_int8(a, sa, torch.tensor([0], **I32), torch.tensor([rows], **I32),
+                               ints(1, 32, K, seed=1), scales(1, 32, seed=2), row_token=index)
     assert (out == 0).all()
 
 
