@@ -48,12 +48,13 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   constexpr int AI = BM / NW / 8, BI = BN / NW / 8;  // 1 KiB loads per wave per K step
   constexpr int kStage = (BM + BN) * kBK;
   constexpr int NO = kGateUp ? BN / 2 : BN;          // output columns of a tile
-  static_assert(AI >= 1 && BI >= 1 && BM % 64 == 0 && BN == 256 && NW > BM / 64, "tile shape");
+  static_assert(AI >= 1 && BI >= 1 && BM % 64 == 0 && NW >= (BM + BN) / 64, "tile shape");
   // separate arrays: the loads into one stage and the reads of the other do not alias
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[kStage];
-  // scales of the tile being computed and of the next: BM rows, then BN rows of B
-  __shared__ __attribute__((aligned(1024))) float scale[2][BM + BN];
+  // scales of three tiles (one wave may still store the last while another loads the
+  // next): BM rows, then BN rows of B
+  __shared__ __attribute__((aligned(1024))) float scale[3][BM + BN];
   __shared__ int pre[kMaxExperts + 1];
   const auto stage = [&](auto S) -> uint8_t* {
     if constexpr (decltype(S)::value % 2 == 0) return lds0;
@@ -165,14 +166,14 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
       load_lds(make_rsrc(src.a, src.abytes), st + (wid * (BM / NW) + 8 * (q - BI)) * kBK,
                lk == KB - 1 && !keep[(q - BI) % AI] ? kOutside : at.a[(q - BI) % AI], lk * kBK);
   };
-  // the scales of the tile whose first K step is loaded, 64 rows a wave, then the columns'
-  auto issue_scales = [&](float* to) __attribute__((always_inline)) {
+  // the scales of a tile, 64 a wave: the rows', then those of B's rows
+  auto issue_scales = [&](const Source& src, const Rows& at, float* to) __attribute__((always_inline)) {
     if (wid < BM / 64) {
       load_lds4(make_rsrc(src.as, src.asbytes), reinterpret_cast<uint8_t*>(to + wid * 64), at.s, 0);
-    } else if (wid == BM / 64) {
-      // four rows of B a lane; gate/up: the second half of the lanes the up rows
-      const uint32_t n = kGateUp && lane >= 32 ? I + 4 * (lane - 32) : 4 * lane;
-      load_lds(make_rsrc(src.bs, src.bsbytes), reinterpret_cast<uint8_t*>(to + BM), n * 4, 0);
+    } else if (wid < (BM + BN) / 64) {
+      const int r = wid * 64 - BM + lane;
+      load_lds4(make_rsrc(src.bs, src.bsbytes), reinterpret_cast<uint8_t*>(to + wid * 64),
+                (uint32_t)(kGateUp && r >= NO ? I + r - NO : r) * 4, 0);
     }
   };
   // K >= 2 steps, so the loads enter the next tile once while a tile is computed
@@ -181,16 +182,11 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
     lk = wrap ? 0 : lk;
     src.a = wrap ? after.a : src.a;
     src.b = wrap ? after.b : src.b;
-    src.as = wrap ? after.as : src.as;
-    src.bs = wrap ? after.bs : src.bs;
     src.abytes = wrap ? after.abytes : src.abytes;
     src.bbytes = wrap ? after.bbytes : src.bbytes;
-    src.asbytes = wrap ? after.asbytes : src.asbytes;
-    src.bsbytes = wrap ? after.bsbytes : src.bsbytes;
     if constexpr (kGather) {
 #pragma unroll
       for (int i = 0; i < AI; ++i) at.a[i] = wrap ? then.a[i] : at.a[i];
-      at.s = wrap ? then.s : at.s;
     }
   };
 
@@ -243,31 +239,34 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   // loads of the next step have landed, there is one barrier; the MFMAs of the last two
   // columns run behind it, so that the first fragments of the next step are read while
   // they do. The loads of the step after next into this stage are spread: kAfter of them
-  // among those MFMAs, the rest over the next step's.
-  constexpr int kAfter = 4;
-  float* next_scale = scale[0];  // where the next tile's go
+  // among those MFMAs, the rest every kEvery-th MFMA of the next step. The order is held by
+  // fences: left to itself the scheduler moves half the loads to the end of the step, next
+  // to their wait, and fragments next to their use (8192 x 4096 x 7168: 203 us; so 187;
+  // all loads behind the barrier 192).
+  constexpr int kAfter = 4, kEvery = 4;
   auto step = [&](auto ml, auto S) __attribute__((always_inline)) {
     constexpr int ML = decltype(ml)::value;
     uint8_t* cur = stage(S);
     uint8_t* nxt = stage(std::integral_constant<int, decltype(S)::value + 1>{});
     constexpr int kBefore = (NI - 2) * ML * 2;  // MFMAs before the barrier
-    if (lk == 0) issue_scales(next_scale);
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int ni = 0; ni < NI - 2; ++ni) {
       fb[(ni + 2) % 4] = read_b(cur, ni + 2);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int mi = 0; mi < ML; ++mi) {
-          const int j = (ni * 2 + h) * ML + mi, q = kAfter + j / 4;
+          const int j = (ni * 2 + h) * ML + mi, q = kAfter + j / kEvery;
           acc[ni][mi] = mfma_int8(fb[ni % 4].h[h], fa[mi].h[h], acc[ni][mi]);
-          if (j % 4 == 0 && q < kLoads) issue(nxt, q);
+          if (j % kEvery == 0 && q < kLoads) issue(nxt, q);
         }
+      __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-    for (int q = kAfter + (kBefore + 3) / 4; q < kLoads; ++q) issue(nxt, q);  // with few MFMAs
+    for (int q = kAfter + (kBefore + kEvery - 1) / kEvery; q < kLoads; ++q) issue(nxt, q);  // with few MFMAs
     next_load();
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
     __syncthreads();
@@ -284,6 +283,7 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
       fa[mi] = read_a(nxt, mi);
       if (mi < 2) fb[mi] = read_b(nxt, mi);
       if (ML == 1) fb[1] = read_b(nxt, 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   // stage of the tile's first step.
   src = after = source_of(tile);
   at = then = rows_of(tile);
-  issue_scales(scale[0]);
+  issue_scales(src, at, scale[0]);
 #pragma unroll
   for (int q = 0; q < kLoads; ++q) issue(lds0, q);
   next_load();
@@ -381,13 +381,13 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   __syncthreads();
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  for (int par = 0, spar = 0;; spar ^= 1) {
+  for (int par = 0, spar = 0;; spar = spar == 2 ? 0 : spar + 1) {
     const Tile ahead = tile_of(place + hop);
     after = source_of(ahead);
     if constexpr (kGather) then = rows_of(ahead);
-    next_scale = scale[spar ^ 1];
     auto compute = [&](auto ml) __attribute__((always_inline)) {
       first_frags(ml, par ? lds1 : lds0);
+      issue_scales(after, then, scale[spar == 2 ? 0 : spar + 1]);
       int kt = 0;
       if (par) {
         step(ml, I1{});
@@ -437,7 +437,7 @@ hipError_t run_gemm(const Int8Rows& a, int64_t rows, int E, const int32_t* offs,
 hipError_t gemm(Out out, const Int8Rows& a, int64_t rows, int E, const int32_t* offs,
                 const int32_t* cnts, const void* w, const float* wsc, int N, int K, void* c,
                 hipStream_t s) {
-  if (gemm_int8_streams(rows, E, K))
+  if (gemm_int8_streams(rows, E, N, K))
     return launch_gemm_int8_stream(out == Out::kGateUp, out != Out::kBF16, a, rows, E, offs, cnts, w,
                                    wsc, N, K, c, s);
   const auto of = [&](auto o) {

@@ -283,10 +283,14 @@ struct Int8Rows {
 hipError_t launch_gemm_int8(const Int8Rows& a, int64_t rows, int E, const int32_t* offs,
                             const int32_t* cnts, const void* w, const float* wsc, int N, int K,
                             int out_dtype, void* out, hipStream_t s);
-// Whether that product (or the gate/up product) streams the weights in 32-row tiles. One K
-// step is too short for the tiled kernel's stream of loads.
-inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t K) {
-  return K <= 128 || rows <= kFewRows * E;
+// Whether that product (or the gate/up product) streams the weights in 32-row tiles: few
+// rows an expert, bound by the weights' bytes either way; or few tiles in all, where the
+// tiled kernel is bound by the latency of its K steps, 31 us for K 4096 however few they
+// are (N 4096, one expert: 64 rows 9.8 against 31 us, 256 rows 17, 512 rows 28, 1024 rows
+// 49 against 33). One K step is too short for the tiled kernel's stream of loads.
+inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t N, int64_t K) {
+  const int64_t padded = rows + 16 * (rows < E ? rows : E);  // the tiles' rows, on average
+  return K <= 128 || rows <= kFewRows * E || padded * N <= (int64_t(1) << 21) + 16 * N;
 }
 // The waves that share one group of weight rows in the streamed kernel, each a part of K:
 // 1 where that already makes two blocks a compute unit (a tile: kStreamRows rows by

@@ -82,12 +82,69 @@ def test_gemm_no_tokens(rows, K):
     assert (out == 0).all()
 
 
-@pytest.mark.parametrize("rows_each", [5, 60, 300])
-def test_gemm_buckets(rows_each):
+# more than 28 rows an expert and 2^21 results: the tiled kernel, tiles of 1 to 256 rows
+TILED = [[700], [255, 256, 257, 64, 65, 128, 129, 1, 0, 300], [1, 1999, 0], [513, 30, 31, 32, 33, 511]]
+
+
+def tiled(rows, E, N, K):
+    return K > 128 and rows > 28 * E and (rows + 16 * min(rows, E)) * N > 2 ** 21 + 16 * N
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts", TILED, ids=str)
+@pytest.mark.parametrize("N,K", [(4112, 144), (4096, 256), (3600, 272), (4368, 1408)])
+def test_gemm_tiled(N, K, counts, dtype):
+    print(f"[gemm int8 tiled] N={N} K={K} counts={counts} {dtype}", flush=True)
+    offs, cnts, rows = buckets(counts)
+    E = len(counts)
+    assert tiled(rows, E, N, K)
+    w, sw = ints(E, N, K, seed=3), scales(E, N, seed=4)
+    check(ints(rows, K, seed=1), scales(rows, seed=2), offs, cnts, w, sw, dtype=dtype)
+    index = torch.randint(0, 37, (rows,), generator=torch.Generator(device=DEV).manual_seed(5),
+                          device=DEV, dtype=torch.int32)
+    for i, bad in enumerate((-1, 37, 2 ** 31 - 1, -2 ** 31, 1 << 28)):
+        index[rows // 5 * i + 1] = bad
+    check(ints(37, K, seed=6), scales(37, seed=7), offs, cnts, w, sw, index=index, dtype=dtype)
+
+
+def test_gemm_tiled_no_tokens():
+    index = torch.zeros(900, **I32)
+    a, sa = torch.empty(0, 1040, device=DEV, dtype=torch.int8), torch.empty(0, device=DEV)
+    out = moe.expert_gemm_int8(a, sa, torch.tensor([0], **I32), torch.tensor([900], **I32),
+                               ints(1, 4096, 1040, seed=1), scales(1, 4096, seed=2), row_token=index)
+    assert tiled(900, 1, 4096, 1040) and (out == 0).all()
+
+
+def test_gemm_tiled_rounds():
+    """More tiles than compute units, with a rest that is cut; rows of all sizes."""
+    g = torch.Generator().manual_seed(1)
+    for E, N, K, most in ((70, 4096, 272, 300), (5, 8208, 400, 2500), (300, 2064, 144, 130)):
+        counts = torch.randint(0, most, (E,), generator=g).tolist()
+        offs, cnts, rows = buckets(counts)
+        assert tiled(rows, E, N, K)
+        check(ints(rows, K, seed=1), scales(rows, seed=2), offs, cnts, ints(E, N, K, seed=3),
+              scales(E, N, seed=4))
+
+
+def test_gemm_tiled_largest_sums():
+    """The longest K, every product the largest, through the tiled kernel."""
+    rows, N, K = 600, 4096, 131056
+    assert tiled(rows, 1, N, K)
+    w = torch.full((1, N, K), -128, device=DEV, dtype=torch.int8)
+    w[0, ::2] = 127
+    offs, cnts, _ = buckets([rows])
+    out = moe.expert_gemm_int8(torch.full((rows, K), -128, device=DEV, dtype=torch.int8),
+                               torch.ones(rows, device=DEV), offs, cnts, w,
+                               torch.ones(1, N, device=DEV), out_dtype=torch.float32)
+    assert (out[:, 1::2] == 16384.0 * K).all() and (out[:, ::2] == -16256.0 * K).all()
+
+
+@pytest.mark.parametrize("N,rows_each", [(144, 5), (144, 60), (144, 300), (2064, 300)])
+def test_gemm_buckets(N, rows_each):
     """Buckets in another order with rows between them; buckets that leave the rows or
     have no sense give nothing; rows in no bucket stay as they were."""
     n = rows_each
-    E, N, K = 9, 144, 272
+    E, K = 9, 272
     rows = 5 * n + 40
     offs = [3 * n + 21, 0, 2 * n + 9, rows - n, -1, rows - n + 1, 0, 2 ** 31 - 1, n + 2]
     cnts = [n, n, n - 1, n, n, n, -4, 2 ** 31 - 1, n - 3]
@@ -186,7 +243,7 @@ def check_ffn(out, d, x, sx, wg, sg, wd, sd):
         assert float(err.max()) <= 0, f"expert {e}: {float(err.max())} over the bound"
 
 
-FFN = [(1, 128, 4, 2, 64), (3, 144, 5, 3, 48), (17, 512, 8, 2, 208), (64, 272, 1, 1, 16),
+FFN = [(3000, 512, 2, 1, 1040), (2500, 1040, 3, 2, 880), (1, 128, 4, 2, 64), (3, 144, 5, 3, 48), (17, 512, 8, 2, 208), (64, 272, 1, 1, 16),
        (40, 256, 64, 8, 1408), (130, 400, 4, 4, 272), (600, 512, 4, 2, 640), (900, 1024, 3, 2, 1040),
        (128, 4096, 16, 8, 1408)]
 
