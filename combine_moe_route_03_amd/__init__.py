@@ -817,6 +817,15 @@ def expert_swiglu_fp8(send_q: torch.Tensor, send_scale: torch.Tensor,
 _Q_CODE = {torch.int8: MOE_I8, _FP8: MOE_F8E4M3}
 
 
+def _rows(shape: torch.Size) -> int:
+    """Rows of a tensor of this shape; they and the columns fit 32 bits."""
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    _int32(rows, shape[-1])
+    return rows
+
+
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
                  residual: torch.Tensor | None = None, q_dtype: torch.dtype | None = None,
                  want_y: bool = True, total: torch.Tensor | None = None,
@@ -827,44 +836,45 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
     sqrt(mean(t^2) + eps) * weight (None unless want_y), q and scale the unrounded y in
     8 bits (None without q_dtype or q): int8 with scale [...], or float8_e4m3fn with
     scale [..., ceil(H/128)]. total and y may be the tensors x and residual."""
-    if x.dtype not in _DTYPE_CODE:
-        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
-    if x.dim() < 1:
+    dev, dt, shape = x.device, x.dtype, x.shape
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
+        raise TypeError(f"x must be float32 or bfloat16, got {dt}")
+    if not shape:
         raise ValueError("x needs at least one dimension")
-    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
     H = shape[-1]
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    _int32(rows, H)
-    if residual is None and total is not None:
+    rows = _rows(shape)
+    at_t = at_r = at_y = at_q = at_s = None
+    if residual is not None:
+        total = _empty(shape, dt, dev) if total is None else total
+        at_r = _checked("residual", residual, shape, dt, dev)
+        at_t = _checked("total", total, shape, dt, dev)
+    elif total is not None:
         raise ValueError("total needs a residual")
-    if residual is not None and total is None:
-        total = _empty(shape, dt, dev)
     if y is None and want_y:
         y = _empty(shape, dt, dev)
+    if y is not None:
+        at_y = _checked("y", y, shape, dt, dev)
     if q is not None:
         if q_dtype is not None and q_dtype != q.dtype:
             raise TypeError(f"q must be {q_dtype}, got {q.dtype}")
         q_dtype = q.dtype
-    if q_dtype is None and scale is not None:
-        raise ValueError("scale needs q or q_dtype")
-    sshape = shape
+    q_code = -1
     if q_dtype is not None:
-        if q_dtype not in _Q_CODE:
+        q_code = _Q_CODE.get(q_dtype)
+        if q_code is None:
             raise TypeError(f"q must be int8 or float8_e4m3fn, got {q_dtype}")
-        sshape = shape[:-1] if q_dtype == torch.int8 else (*shape[:-1], _blocks(H))
+        sshape = shape[:-1] if q_code == MOE_I8 else (*shape[:-1], _blocks(H))
         q = _empty(shape, q_dtype, dev) if q is None else q
         scale = _empty(sshape, torch.float32, dev) if scale is None else scale
-
-    def at(name, t, shape, dtype):
-        return None if t is None else _checked(name, t, shape, dtype, dev)
-
+        at_q = _checked("q", q, shape, q_dtype, dev)
+        at_s = _checked("scale", scale, sshape, torch.float32, dev)
+    elif scale is not None:
+        raise ValueError("scale needs q or q_dtype")
     _check(lib().moe_add_rms_norm(
-        _DTYPE_CODE[dt], _Q_CODE.get(q_dtype, -1), rows, H, _checked("x", x, shape, dt, dev),
-        at("residual", residual, shape, dt), _checked("weight", weight, (H,), dt, dev), eps,
-        at("total", total, shape, dt), at("y", y, shape, dt), at("q", q, shape, q_dtype),
-        at("scale", scale, sshape, torch.float32), _current_stream(dev)), "moe_add_rms_norm")
+        code, q_code, rows, H, _checked("x", x, shape, dt, dev), at_r,
+        _checked("weight", weight, (H,), dt, dev), eps, at_t, at_y, at_q, at_s,
+        _current_stream(dev)), "moe_add_rms_norm")
     return total, y, q, scale
 
 
@@ -876,12 +886,9 @@ def quantize_int8(x: torch.Tensor, q: torch.Tensor | None = None,
         raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
     if x.dim() < 1:
         raise ValueError("x needs at least one dimension")
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     cols = shape[-1]
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    _int32(rows, cols)
+    rows = _rows(shape)
     q = _empty(shape, torch.int8, dev) if q is None else q
     scale = _empty(shape[:-1], torch.float32, dev) if scale is None else scale
     _check(lib().moe_quantize_int8(

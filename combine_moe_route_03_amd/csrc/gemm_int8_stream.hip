@@ -107,6 +107,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
   constexpr int kGroupCols = kGateUp ? 16 : 32;
   constexpr int kNO = kGroups * kGroupCols;  // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][kStageBytes];
+  __shared__ __attribute__((aligned(16))) float row_scale[kWave], col_scale[kStreamCols];
   __shared__ int info[4];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -132,11 +133,25 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
   }
   const int wrow[2] = {kGateUp ? 4 * (lr >> 1) + (lr & 1) : lr,
                        kGateUp ? 4 * (lr >> 1) + (lr & 1) + 2 : 8 + lr};
-  // the row of A behind row m of the tile (tokens where there is none)
+  // the row of A behind row m of the tile (past the last one where there is none)
   const auto source = [&](int m) -> uint32_t {
     if (m >= rows) return tokens;
     return idx ? (uint32_t)idx[row0 + m] : (uint32_t)(row0 + m);
   };
+  // The tile's scales go straight into LDS, where they are when the products are: rows of
+  // w by waves 0 and up (gate/up: the gate rows, then the up rows), rows of A by the last.
+  constexpr int kWRows = kStreamCols / WK;
+  if (wid * kWave < kWRows) {
+    const int r = wid * kWave + lane, c = kGateUp && r >= kNO ? r - kNO : r;
+    const int n = tile.ntile * kNO + c + (kGateUp && r >= kNO ? I : 0);
+    load_lds4(make_rsrc(Bsc + (int64_t)e * N, (int64_t)N * 4),
+              reinterpret_cast<uint8_t*>(col_scale + wid * kWave), r < kWRows ? n * 4 : kOutside, 0);
+  }
+  if (wid == kWaves - 1) {
+    const uint32_t r = source(lane);
+    load_lds4(make_rsrc(Asc, (int64_t)tokens * 4), reinterpret_cast<uint8_t*>(row_scale),
+              r < tokens ? r * 4 : kOutside, 0);
+  }
 
   auto pass = [&](auto nb_, auto shared) __attribute__((always_inline)) {
     constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
@@ -160,22 +175,20 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
     const auto emit = [&](int f, int t, i32x4 v) __attribute__((always_inline)) {
       const int m = 16 * t + i;
       if (m >= rows || (NB == 1 && i >= 8)) return;
-      const uint32_t r = source(m);
-      const float sa = r < tokens ? Asc[r] : 0.f;
-      const float* ws = Bsc + (int64_t)e * N;
+      const float sa = row_scale[m];
       if constexpr (kGateUp) {
-        const int n = n0 + 8 * f + 2 * g;
+        const int c = group * kGroupCols + 8 * f + 2 * g, n = tile.ntile * kNO + c;
         if (n >= I) return;
-        const float2 sg = *reinterpret_cast<const float2*>(ws + n);
-        const float2 su = *reinterpret_cast<const float2*>(ws + I + n);
+        const float2 sg = *reinterpret_cast<const float2*>(col_scale + c);
+        const float2 su = *reinterpret_cast<const float2*>(col_scale + kNO + c);
         float2 h;
         h.x = silu(scaled(v[0], sa, sg.x)) * scaled(v[2], sa, su.x);
         h.y = silu(scaled(v[1], sa, sg.y)) * scaled(v[3], sa, su.y);
         *reinterpret_cast<float2*>(static_cast<float*>(C) + (int64_t)(row0 + m) * I + n) = h;
       } else {
-        const int n = n0 + 16 * f + 4 * g;
+        const int c = group * kGroupCols + 16 * f + 4 * g, n = tile.ntile * kNO + c;
         if (n >= N) return;
-        const float4 sw = *reinterpret_cast<const float4*>(ws + n);
+        const float4 sw = *reinterpret_cast<const float4*>(col_scale + c);
         const float o[4] = {scaled(v[0], sa, sw.x), scaled(v[1], sa, sw.y), scaled(v[2], sa, sw.z),
                             scaled(v[3], sa, sw.w)};
         const int64_t at = (int64_t)(row0 + m) * N + n;
@@ -186,26 +199,22 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
               make_uint2(bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3]));
       }
     };
-    if constexpr (WK == 1) {
+    // Every wave's sums in its stage, of which the group's waves then take the fragments
+    // in turn (also a wave alone: results straight from the registers made it spill).
+    constexpr int kFrags = 2 * NTL;
+    i32x4* own = reinterpret_cast<i32x4*>(stage[wid]);
+    static_assert(kFrags * kWave * 16 <= kStageBytes, "sums fit the stage");
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+    for (int j = 0; j < kFrags; ++j) own[j * kWave + lane] = acc[j / NTL][j % NTL];
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // the scales
+    __syncthreads();
+#pragma unroll 1
+    for (int j = part; j < kFrags; j += WK) {
+      i32x4 v = {0, 0, 0, 0};
 #pragma unroll
-        for (int t = 0; t < NTL; ++t) emit(f, t, acc[f][t]);
-    } else {
-      // every wave's sums behind its stage; the group's waves share the fragments
-      constexpr int kFrags = 2 * NTL;
-      i32x4* own = reinterpret_cast<i32x4*>(stage[wid]);
-      static_assert(kFrags * kWave * 16 <= kStageBytes, "sums fit the stage");
-#pragma unroll
-      for (int j = 0; j < kFrags; ++j) own[j * kWave + lane] = acc[j / NTL][j % NTL];
-      __syncthreads();
-      for (int j = part; j < kFrags; j += WK) {
-        i32x4 v = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < WK; ++w)
-          v += reinterpret_cast<const i32x4*>(stage[group * WK + w])[j * kWave + lane];
-        emit(j / NTL, j % NTL, v);
-      }
+      for (int w = 0; w < WK; ++w)
+        v += reinterpret_cast<const i32x4*>(stage[group * WK + w])[j * kWave + lane];
+      emit(j / NTL, j % NTL, v);
     }
   };
   // the expert's other tiles read the same weights

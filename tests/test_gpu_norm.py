@@ -51,6 +51,19 @@ def test_widths(H, dtype, q_dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [48, 144, 272, 528, 784, 1040, 1408, 2064, 2832, 4080, 4112, 8192])
+def test_rows_of_a_wave(H, dtype):
+    """From 1024 rows on a wave takes a row, up to eight vectors a lane."""
+    for T, add, q_dtype in ((1024, True, torch.int8), (1027, False, E4M3), (1030, True, None)):
+        x, r = hidden(T, H, dtype, 21), hidden(T, H, dtype, 22) if add else None
+        w = (1 + 0.3 * torch.randn(H, device=DEV)).to(dtype)
+        check_norm(x, w, 1e-5, r, q_dtype, moe.add_rms_norm(x, w, 1e-5, residual=r, q_dtype=q_dtype))
+    q, scale = moe.quantize_int8(x)
+    want_q, want_s = ref.int8_rows(x)
+    assert torch.equal(scale.double(), want_s) and torch.equal(q.double(), want_q)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_many_rows(dtype):
     """More rows than a wave of blocks, past the size up to which results are cached."""
     T, H = (24001, 4096) if dtype == BF16 else (9001, 4096)
@@ -118,10 +131,10 @@ def test_values_at_the_ends(H, dtype):
     check_norm(x[keep], w, 0.0, None, torch.int8, (None, y[keep], q[keep], scale[keep]))
 
 
-@pytest.mark.parametrize("H", [128, 512, 4096])
-def test_infinities_and_nan(H):
+@pytest.mark.parametrize("T,H", [(6, 128), (6, 512), (6, 4096), (1050, 512), (1050, 2048), (1050, 8192)])
+def test_infinities_and_nan(T, H):
     inf, nan = float("inf"), float("nan")
-    x = hidden(6, H, BF16, 10)
+    x = hidden(T, H, BF16, 10)
     w = (1 + 0.1 * torch.randn(H, device=DEV)).to(BF16)
     clean = moe.add_rms_norm(x, w, 1e-6, q_dtype=torch.int8)
     clean8 = moe.add_rms_norm(x, w, 1e-6, q_dtype=E4M3)
@@ -136,7 +149,7 @@ def test_infinities_and_nan(H):
     y8, q8, s8 = moe.add_rms_norm(bad, w, 1e-6, q_dtype=E4M3)[1:]
     assert q8[1, 5].float().isnan() and (q8[1, :5].float() == 0).all() and s8[1, 0] == 1
     assert q8[3].float().isnan().all()
-    for i in (0, 2, 4, 5):
+    for i in (0, 2, 4, 5, T - 1):
         assert torch.equal(y[i], clean[1][i]) and torch.equal(q[i], clean[2][i])
         assert torch.equal(q8[i].view(torch.uint8), clean8[2][i].view(torch.uint8))
     # an infinite weight: infinities saturate, the others keep the scale of the finite ones
