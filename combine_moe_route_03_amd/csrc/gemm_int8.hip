@@ -31,12 +31,21 @@ enum class Out { kBF16, kF32, kGateUp };
 // the rows run with one or two fragments a wave. N: rows of one expert's B (2 I
 // for gate/up). One block a compute unit; it takes every gridDim.x / 8-th tile of
 // its XCD's share of the list (contiguous, so the XCD's L2 serves its rows and
-// weights), and the K steps of its tiles are one stream: the loads run two steps
+// weights), and the K steps of its tiles are one stream: the loads run NS steps
 // ahead, into the next tile's first steps while this one's last run and its results are
 // stored. The tiles of an XCD's last, partial round are cut into two or four by
 // rows where that still gives each unit one, and come first: blocks then end their
 // tiles, and store, at different times.
-template <Out kOut, bool kGather, int BM, int BN, int WM, int WN>
+//
+// Two shapes. 256 x 256, two stages: the fewest loads a product, for many rows. The K loop
+// runs at 2.5-2.8 POP/s, the matrix pipes 71% busy, and the clock falls from 2.4 to 1.9 GHz
+// under it: power bounds it, so what saves energy counts (the 32 x 32 x 32 instruction,
+// with twice the sums' traffic a product, ran at 1.7 GHz: 213 against 187 us for 8192 x
+// 4096 x 7168; 4 waves of 128 x 128 spill: 222). 128 x 256, three stages: twice the time for
+// a load to land, for few tiles, whose steps are as long as a load takes (0.95 us with two
+// stages, 0.5 with three: 1024 x 4096 x 4096 32 against 23 us), and for short experts; with
+// many rows its 1.5 times the loads cost more than it gains (8192 rows 212 against 190 us).
+template <Out kOut, bool kGather, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ Asc, const int32_t* __restrict__ idx,
     uint32_t tokens, const int32_t* __restrict__ offs, const int32_t* __restrict__ cnts, int E,
@@ -52,13 +61,16 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   // separate arrays: the loads into one stage and the reads of the other do not alias
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[NS == 3 ? kStage : 16];
   // scales of three tiles (one wave may still store the last while another loads the
   // next): BM rows, then BN rows of B
   __shared__ __attribute__((aligned(1024))) float scale[3][BM + BN];
   __shared__ int pre[kMaxExperts + 1];
   const auto stage = [&](auto S) -> uint8_t* {
-    if constexpr (decltype(S)::value % 2 == 0) return lds0;
-    else return lds1;
+    constexpr int V = decltype(S)::value % NS;
+    if constexpr (V == 0) return lds0;
+    else if constexpr (V == 1) return lds1;
+    else return lds2;
   };
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -176,7 +188,7 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
                 (uint32_t)(kGateUp && r >= NO ? I + r - NO : r) * 4, 0);
     }
   };
-  // K >= 2 steps, so the loads enter the next tile once while a tile is computed
+  // K >= NS steps, so the loads enter the next tile once while a tile is computed
   auto next_load = [&]() __attribute__((always_inline)) {
     const bool wrap = ++lk == KB;
     lk = wrap ? 0 : lk;
@@ -221,33 +233,32 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   Tile tile = tile_of(place);
   i32x4 acc[NI][MI];
   Frag fa[MI], fb[4];
-  // ML: the wave's row fragments in use
-  auto first_frags = [&](auto ml, const uint8_t* st) __attribute__((always_inline)) {
-    constexpr int ML = decltype(ml)::value;
+  // The first fragments of a step: all of A's, whichever tile comes next.
+  auto first_frags = [&](const uint8_t* st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int mi = 0; mi < ML; ++mi) fa[mi] = read_a(st, mi);
+    for (int mi = 0; mi < MI; ++mi) fa[mi] = read_a(st, mi);
     fb[0] = read_b(st, 0);
     fb[1] = read_b(st, 1);
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-      for (int mi = 0; mi < ML; ++mi) acc[ni][mi] = i32x4{0, 0, 0, 0};
   };
 
   // A step reads stage S. Its fragments of A and the first two fragments of B are in
   // registers already. Once a wave has read the last fragments of the stage and its
   // loads of the next step have landed, there is one barrier; the MFMAs of the last two
   // columns run behind it, so that the first fragments of the next step are read while
-  // they do. The loads of the step after next into this stage are spread: kAfter of them
-  // among those MFMAs, the rest every kEvery-th MFMA of the next step. The order is held by
+  // they do. The loads of the step NS on into this stage are spread: kAfter of them
+  // among those MFMAs, the rest every kEvery-th MFMA of the next step. With three stages
+  // those of one more step may be pending at the barrier, and, in a tile's first step
+  // (behind), the last tile's stores, which were issued among them. The order is held by
   // fences: left to itself the scheduler moves half the loads to the end of the step, next
   // to their wait, and fragments next to their use (8192 x 4096 x 7168: 203 us; so 187;
   // all loads behind the barrier 192).
-  constexpr int kAfter = 4, kEvery = 4;
-  auto step = [&](auto ml, auto S) __attribute__((always_inline)) {
-    constexpr int ML = decltype(ml)::value;
+  constexpr int kAfter = kLoads / 2, kEvery = 4;
+  constexpr int kLeast = (kOut == Out::kF32 ? NI : NI / 2) * (MI / 4);  // stores of a tile
+  auto step = [&](auto ml, auto S, bool behind) __attribute__((always_inline)) {
+    constexpr int ML = decltype(ml)::value, V = decltype(S)::value;
     uint8_t* cur = stage(S);
-    uint8_t* nxt = stage(std::integral_constant<int, decltype(S)::value + 1>{});
+    uint8_t* nxt = stage(std::integral_constant<int, V + 1>{});
+    uint8_t* end = stage(std::integral_constant<int, V + NS - 1>{});
     constexpr int kBefore = (NI - 2) * ML * 2;  // MFMAs before the barrier
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -260,16 +271,21 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
         for (int mi = 0; mi < ML; ++mi) {
           const int j = (ni * 2 + h) * ML + mi, q = kAfter + j / kEvery;
           acc[ni][mi] = mfma_int8(fb[ni % 4].h[h], fa[mi].h[h], acc[ni][mi]);
-          if (j % kEvery == 0 && q < kLoads) issue(nxt, q);
+          if (j % kEvery == 0 && q < kLoads) issue(end, q);
         }
       __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-    for (int q = kAfter + (kBefore + kEvery - 1) / kEvery; q < kLoads; ++q) issue(nxt, q);  // with few MFMAs
+    for (int q = kAfter + (kBefore + kEvery - 1) / kEvery; q < kLoads; ++q) issue(end, q);  // with few MFMAs
     next_load();
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-    __syncthreads();
+    if constexpr (NS == 2) {
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    } else {
+      if (behind) __builtin_amdgcn_s_waitcnt(wait_vmcnt(kLoads + kLeast));
+      else __builtin_amdgcn_s_waitcnt(wait_vmcnt(kLoads));
+    }
+    lds_barrier();
 #pragma unroll
     for (int mi = 0; mi < ML; ++mi) {
 #pragma unroll
@@ -284,6 +300,10 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
       if (mi < 2) fb[mi] = read_b(nxt, mi);
       if (ML == 1) fb[1] = read_b(nxt, 1);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (NS == 3) {
+#pragma unroll
+      for (int mi = ML; mi < MI; ++mi) fa[mi] = read_a(nxt, mi);
     }
   };
 
@@ -367,46 +387,80 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
       }
     }
   };
-  // Steps 0 and (the first kAfter loads) 1 of the stream, then tile by tile; par: the
+  // The first NS - 1 steps and the first kAfter loads of one more, then tile by tile; par: the
   // stage of the tile's first step.
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
   src = after = source_of(tile);
   at = then = rows_of(tile);
   issue_scales(src, at, scale[0]);
 #pragma unroll
   for (int q = 0; q < kLoads; ++q) issue(lds0, q);
   next_load();
+  if constexpr (NS == 3) {
 #pragma unroll
-  for (int q = 0; q < kAfter; ++q) issue(lds1, q);
-  __builtin_amdgcn_s_waitcnt(wait_vmcnt(kAfter));
+    for (int q = 0; q < kLoads; ++q) issue(lds1, q);
+    next_load();
+  }
+#pragma unroll
+  for (int q = 0; q < kAfter; ++q) issue(NS == 3 ? lds2 : lds1, q);
+  __builtin_amdgcn_s_waitcnt(wait_vmcnt(kLoads * (NS - 2) + kAfter));
   __syncthreads();
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
+  if constexpr (NS == 3) first_frags(lds0);
+  bool behind = false;  // a tile's stores are behind the loads of the next step
   for (int par = 0, spar = 0;; spar = spar == 2 ? 0 : spar + 1) {
     const Tile ahead = tile_of(place + hop);
     after = source_of(ahead);
     if constexpr (kGather) then = rows_of(ahead);
     auto compute = [&](auto ml) __attribute__((always_inline)) {
-      first_frags(ml, par ? lds1 : lds0);
+      constexpr int ML = decltype(ml)::value;
+      if constexpr (NS == 2) first_frags(par ? lds1 : lds0);
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < ML; ++mi) acc[ni][mi] = i32x4{0, 0, 0, 0};
       issue_scales(after, then, scale[spar == 2 ? 0 : spar + 1]);
       int kt = 0;
-      if (par) {
-        step(ml, I1{});
-        ++kt;
+      if constexpr (NS == 2) {
+        if (par) {
+          step(ml, I1{}, false);
+          ++kt;
+        }
+        for (; kt + 2 <= KB; kt += 2) {
+          step(ml, I0{}, false);
+          step(ml, I1{}, false);
+        }
+        if (kt < KB) step(ml, I0{}, false);
+        // The loads that run ahead land here, where it costs the least: past this point
+        // nothing is pending in either stage, whichever the next tile begins with.
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+      } else {
+        if (par == 1) {
+          step(ml, I1{}, behind);
+          step(ml, I2{}, false);
+          kt = 2;
+        } else if (par == 2) {
+          step(ml, I2{}, behind);
+          kt = 1;
+        }
+        for (; kt + 3 <= KB; kt += 3) {
+          step(ml, I0{}, behind && kt == 0);
+          step(ml, I1{}, false);
+          step(ml, I2{}, false);
+        }
+        if (kt < KB) {
+          step(ml, I0{}, false);
+          if (kt + 1 < KB) step(ml, I1{}, false);
+        }
       }
-      for (; kt + 2 <= KB; kt += 2) {
-        step(ml, I0{});
-        step(ml, I1{});
-      }
-      if (kt < KB) step(ml, I0{});
-      // The loads that run ahead land here, where it costs the least: past this point
-      // nothing is pending in either stage, whichever the next tile begins with.
-      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
       finish(ml, scale[spar]);
     };
     if (tile.rows > BM / 2) compute(std::integral_constant<int, MI>{});
     else if (tile.rows > BM / 4) compute(std::integral_constant<int, MI / 2>{});
     else compute(std::integral_constant<int, MI / 4>{});
-    par = (par + KB) & 1;
+    par = (par + KB) % NS;
+    behind = true;
     place += hop;
     if (place >= limit) break;
     tile = ahead;
@@ -415,11 +469,11 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
 }
 
-template <Out kOut, bool kGather>
+template <Out kOut, bool kGather, int BM, int WM, int WN, int NS>
 hipError_t run_gemm(const Int8Rows& a, int64_t rows, int E, const int32_t* offs,
                     const int32_t* cnts, const void* w, const float* wsc, int N, int K, void* c,
                     hipStream_t s) {
-  constexpr int BM = 256, BN = 256;
+  constexpr int BN = 256;
   constexpr int NO = kOut == Out::kGateUp ? BN / 2 : BN;
   const int cols = kOut == Out::kGateUp ? N / 2 : N;
   const int ntiles = (cols + NO - 1) / NO;
@@ -428,7 +482,7 @@ hipError_t run_gemm(const Int8Rows& a, int64_t rows, int E, const int32_t* offs,
   // one block a compute unit (a tile alone on its XCD is cut into four)
   int64_t per = 4 * ((mt * ntiles + kXCD - 1) / kXCD);
   if (per > kUnitsPerXcd) per = kUnitsPerXcd;
-  return launch(gemm_int8_kernel<kOut, kGather, BM, BN, 4, 2>, dim3((unsigned)(per * kXCD)),
+  return launch(gemm_int8_kernel<kOut, kGather, BM, BN, WM, WN, NS>, dim3((unsigned)(per * kXCD)),
                 dim3(kWave * 8), 0, s, static_cast<const uint8_t*>(a.q), a.scale, a.index,
                 (uint32_t)a.rows, offs, cnts, E, rows, static_cast<const uint8_t*>(w), wsc, N, K, c,
                 ntiles);
@@ -440,10 +494,17 @@ hipError_t gemm(Out out, const Int8Rows& a, int64_t rows, int E, const int32_t* 
   if (gemm_int8_streams(rows, E, N, K))
     return launch_gemm_int8_stream(out == Out::kGateUp, out != Out::kBF16, a, rows, E, offs, cnts, w,
                                    wsc, N, K, c, s);
+  // tiles of 256 rows, on average half a one more an expert; the stream of loads is at
+  // least as many steps long as there are stages
+  const int64_t tiles = (rows / 256 + (rows < E ? rows : E)) * ((N + 255) / 256);
+  const bool small = K > 256 && (rows <= (int64_t)128 * E || tiles <= 160);
   const auto of = [&](auto o) {
     constexpr Out O = decltype(o)::value;
-    return a.index ? run_gemm<O, true>(a, rows, E, offs, cnts, w, wsc, N, K, c, s)
-                   : run_gemm<O, false>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
+    if (small)
+      return a.index ? run_gemm<O, true, 128, 2, 4, 3>(a, rows, E, offs, cnts, w, wsc, N, K, c, s)
+                     : run_gemm<O, false, 128, 2, 4, 3>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
+    return a.index ? run_gemm<O, true, 256, 4, 2, 2>(a, rows, E, offs, cnts, w, wsc, N, K, c, s)
+                   : run_gemm<O, false, 256, 4, 2, 2>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
   };
   if (out == Out::kGateUp) return of(std::integral_constant<Out, Out::kGateUp>{});
   return out == Out::kF32 ? of(std::integral_constant<Out, Out::kF32>{})

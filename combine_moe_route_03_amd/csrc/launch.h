@@ -284,21 +284,23 @@ hipError_t launch_gemm_int8(const Int8Rows& a, int64_t rows, int E, const int32_
                             const int32_t* cnts, const void* w, const float* wsc, int N, int K,
                             int out_dtype, void* out, hipStream_t s);
 // Whether that product (or the gate/up product) streams the weights in 32-row tiles: few
-// rows an expert, bound by the weights' bytes either way; or few tiles in all, where the
-// tiled kernel is bound by the latency of its K steps, 31 us for K 4096 however few they
-// are (N 4096, one expert: 64 rows 9.8 against 31 us, 256 rows 17, 512 rows 28, 1024 rows
-// 49 against 33). One K step is too short for the tiled kernel's stream of loads.
+// rows an expert, bound by the weights' bytes either way; or few results in all, where the
+// tiled kernel is bound by the latency of its K steps, 19 us for K 4096 however few they
+// are (N 4096, one expert: 64 rows 9.6 against 19 us, 128 rows 12, 256 rows 17, 384 rows
+// 26). One K step is too short for the tiled kernel's stream of loads.
 inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int64_t padded = rows + 16 * (rows < E ? rows : E);  // the tiles' rows, on average
-  return K <= 128 || rows <= kFewRows * E || padded * N <= (int64_t(1) << 21) + 16 * N;
+  return K <= 128 || rows <= kFewRows * E || padded * N <= (int64_t(1) << 20) + 16 * N;
 }
 // The waves that share one group of weight rows in the streamed kernel, each a part of K:
-// 1 where that already makes two blocks a compute unit (a tile: kStreamRows rows by
-// kStreamCols / parts), more where it does not.
+// as many as make one and a half blocks a compute unit (a tile: kStreamRows rows by
+// kStreamCols / parts). Two fit; asking for two splits 448 blocks in halves that take two
+// rounds (200 rows, N 4096, K 4096: 21 against 17 us), asking for one leaves units with
+// half their waves (40 rows of 16 experts, N 2816: 35 against 30).
 inline int gemm_int8_splits(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int64_t mt = rows / kStreamRows + (rows < E ? rows : E);
   int parts = 1;
-  while (parts < 8 && K > 256 * parts && mt * ((N * parts + kStreamCols - 1) / kStreamCols) < 512)
+  while (parts < 8 && K > 256 * parts && mt * ((N * parts + kStreamCols - 1) / kStreamCols) < 400)
     parts *= 2;
   return parts;
 }

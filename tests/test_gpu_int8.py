@@ -82,17 +82,20 @@ def test_gemm_no_tokens(rows, K):
     assert (out == 0).all()
 
 
-# more than 28 rows an expert and 2^21 results: the tiled kernel, tiles of 1 to 256 rows
-TILED = [[700], [255, 256, 257, 64, 65, 128, 129, 1, 0, 300], [1, 1999, 0], [513, 30, 31, 32, 33, 511]]
+# more than 28 rows an expert and 2^20 results: the tiled kernel, tiles of 1 to 256 rows;
+# of up to 128 where there are few tiles or rows an expert and more than two K steps
+TILED = [[700], [255, 256, 257, 64, 65, 128, 129, 1, 0, 300], [1, 1999, 0], [513, 30, 31, 32, 33, 511],
+         [2047, 1, 897, 95, 0, 160], [33] * 40 + [127, 0, 31, 3]]
 
 
 def tiled(rows, E, N, K):
-    return K > 128 and rows > 28 * E and (rows + 16 * min(rows, E)) * N > 2 ** 21 + 16 * N
+    return K > 128 and rows > 28 * E and (rows + 16 * min(rows, E)) * N > 2 ** 20 + 16 * N
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("counts", TILED, ids=str)
-@pytest.mark.parametrize("N,K", [(4112, 144), (4096, 256), (3600, 272), (4368, 1408)])
+@pytest.mark.parametrize("N,K", [(4112, 144), (4096, 256), (3600, 272), (4368, 1408), (8208, 400),
+                                 (2064, 528)])
 def test_gemm_tiled(N, K, counts, dtype):
     print(f"[gemm int8 tiled] N={N} K={K} counts={counts} {dtype}", flush=True)
     offs, cnts, rows = buckets(counts)
@@ -107,12 +110,13 @@ def test_gemm_tiled(N, K, counts, dtype):
     check(ints(37, K, seed=6), scales(37, seed=7), offs, cnts, w, sw, index=index, dtype=dtype)
 
 
-def test_gemm_tiled_no_tokens():
-    index = torch.zeros(900, **I32)
+@pytest.mark.parametrize("rows", [900, 4000])
+def test_gemm_tiled_no_tokens(rows):
+    index = torch.zeros(rows, **I32)
     a, sa = torch.empty(0, 1040, device=DEV, dtype=torch.int8), torch.empty(0, device=DEV)
-    out = moe.expert_gemm_int8(a, sa, torch.tensor([0], **I32), torch.tensor([900], **I32),
+    out = moe.expert_gemm_int8(a, sa, torch.tensor([0], **I32), torch.tensor([rows], **I32),
                                ints(1, 4096, 1040, seed=1), scales(1, 4096, seed=2), row_token=index)
-    assert tiled(900, 1, 4096, 1040) and (out == 0).all()
+    assert tiled(rows, 1, 4096, 1040) and (out == 0).all()
 
 
 def test_gemm_tiled_rounds():
@@ -126,9 +130,10 @@ def test_gemm_tiled_rounds():
               scales(E, N, seed=4))
 
 
-def test_gemm_tiled_largest_sums():
+@pytest.mark.parametrize("rows", [600, 3000])
+def test_gemm_tiled_largest_sums(rows):
     """The longest K, every product the largest, through the tiled kernel."""
-    rows, N, K = 600, 4096, 131056
+    N, K = 4096, 131056
     assert tiled(rows, 1, N, K)
     w = torch.full((1, N, K), -128, device=DEV, dtype=torch.int8)
     w[0, ::2] = 127
