@@ -296,7 +296,7 @@ __global__ __launch_bounds__(G ? kPackThreads : 1024) void quantize_int8_kernel(
       int b[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        b[k] = int8_round((double)__builtin_amdgcn_fmed3f(t[j].get(4 * i + k), -most, most), inv);
+        b[k] = int8_round_exact(__builtin_amdgcn_fmed3f(t[j].get(4 * i + k), -most, most), inv);
       o[i] = pack_int8(b[0], b[1], b[2], b[3]);
     }
     if (live && c < nvec) put_q<kCache>(q + (base + c) * N, o);

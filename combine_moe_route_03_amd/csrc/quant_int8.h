@@ -16,14 +16,19 @@ __device__ __forceinline__ float int8_scale(double amax) {
   return s < 0x1p-126 ? 0x1p-126f : (s > 3.4028234663852886e38 ? 3.4028234663852886e38f : (float)s);
 }
 
-// v / scale to the nearest integer, |v| <= 127 scale; inv = 1 / scale, rounded to 64 bits.
-// The first sum leaves multiples of 2^-32, the second integers, each rounding to nearest
-// even; the integer is then the low word. Fp32 v and scale: a quotient that is not half
-// way between two integers is at least 2^-25 from there, and one that is comes out so
-// although inv is rounded, so the result is that of the exact quotient.
+// v / scale to the nearest integer, |v| <= 127 scale; inv = 1 / scale, rounded to 64 bits. The
+// sum leaves an integer, rounded to nearest even, in the low word.
+//
+// Any v: off by inv's rounding, 2^-46 of a step at most.
 __device__ __forceinline__ int int8_round(double v, double inv) {
+  return (int)(uint32_t)__double_as_longlong(__builtin_fma(v, inv, 0x1.8p52));
+}
+// Fp32 v and scale: the result of the exact quotient. One that is not half way between two
+// integers is at least 2^-25 from there; the first sum leaves multiples of 2^-32, so one
+// that is comes out so although inv is rounded.
+__device__ __forceinline__ int int8_round_exact(float v, double inv) {
   constexpr double kFine = 0x1.8p20, kWhole = 0x1.8p52;
-  const double fine = __builtin_fma(v, inv, kFine);
+  const double fine = __builtin_fma((double)v, inv, kFine);
   return (int)(uint32_t)__double_as_longlong(fine + (kWhole - kFine));
 }
 

@@ -167,6 +167,33 @@ def test_infinities_and_nan(T, H):
     assert torch.equal(q[live], q0[live])
 
 
+@pytest.mark.parametrize("T", [1, 1030])
+def test_int8_next_to_a_border(T):
+    """Quotients 2^-37 to 2^-44 off the middle of two integers land on their own side: t w is
+    the product of two 24-bit integers next to (2 n + 1) 2^44, the row's norm a power of two."""
+    g = torch.Generator().manual_seed(17)
+    a = torch.randint(1 << 23, 1 << 24, (1 << 21,), generator=g)
+    t, w, want = [127.0], [1.0], [127]
+    for n in range(1, 8):
+        m = (2 * n + 1) << 44
+        b = (m + a // 2) // a
+        d = a * b - m
+        for below in (True, False):
+            ok = (d < 0 if below else d > 0) & (d.abs() < 256) & (b < 1 << 24)
+            i = int(ok.nonzero()[0])
+            for sign in (1, -1):
+                t.append(sign * float(a[i]) * 2.0 ** -23)
+                w.append(float(b[i]) * 2.0 ** -22)
+                want.append(sign * (n if below else n + 1))
+    t, w = torch.tensor(t + [0.0] * 3, dtype=F32), torch.tensor(w + [1.0] * 3, dtype=F32)
+    assert t.numel() == 32
+    eps = 1024.0 - float((t.double() ** 2).mean())
+    x = t.to(DEV).repeat(T, 1)
+    _, _, q, scale = moe.add_rms_norm(x, w.to(DEV), eps, q_dtype=torch.int8)
+    assert (scale == 2.0 ** -5).all()
+    assert torch.equal(q.cpu(), torch.tensor(want + [0] * 3, dtype=torch.int8).repeat(T, 1))
+
+
 # ------------------------------------------------------------------ quantize_int8
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
