@@ -108,10 +108,13 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
   constexpr int kNO = kGroups * kGroupCols;  // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][kStageBytes];
   __shared__ __attribute__((aligned(16))) float row_scale[kWave], col_scale[kStreamCols];
-  __shared__ int info[4];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const Tile tile = find_tile<kRows>(offs, cnts, E, rows_total, ntiles, info);
+  const WaveTile tile =
+      E <= kWave       ? find_tile_wave<kRows, 1>(offs, cnts, E, rows_total, ntiles)
+      : E <= 2 * kWave ? find_tile_wave<kRows, 2>(offs, cnts, E, rows_total, ntiles)
+      : E <= 4 * kWave ? find_tile_wave<kRows, 4>(offs, cnts, E, rows_total, ntiles)
+                       : find_tile_wave<kRows, kMaxExperts / kWave>(offs, cnts, E, rows_total, ntiles);
   if (tile.e < 0) return;  // uniform over the block
   const int e = tile.e, row0 = tile.row0, rows = tile.rows;
   const int i = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
@@ -218,7 +221,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
     }
   };
   // the expert's other tiles read the same weights
-  if (cnts[e] > kRows) pass(std::integral_constant<int, 4>{}, std::true_type{});
+  if (tile.len > kRows) pass(std::integral_constant<int, 4>{}, std::true_type{});
   else if (rows <= 8) pass(std::integral_constant<int, 1>{}, std::false_type{});
   else if (rows <= 16) pass(std::integral_constant<int, 2>{}, std::false_type{});
   else pass(std::integral_constant<int, 4>{}, std::false_type{});

@@ -292,15 +292,19 @@ inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int64_t padded = rows + 16 * (rows < E ? rows : E);  // the tiles' rows, on average
   return K <= 128 || rows <= kFewRows * E || padded * N <= (int64_t(1) << 20) + 16 * N;
 }
-// The waves that share one group of weight rows in the streamed kernel, each a part of K:
-// as many as make one and a half blocks a compute unit (a tile: kStreamRows rows by
-// kStreamCols / parts). Two fit; asking for two splits 448 blocks in halves that take two
-// rounds (200 rows, N 4096, K 4096: 21 against 17 us), asking for one leaves units with
-// half their waves (40 rows of 16 experts, N 2816: 35 against 30).
+// The waves that share one group of weight rows in the streamed kernel, each a part of K
+// (a tile: kStreamRows rows by kStreamCols / parts): as many as give every compute unit a
+// block, or one and a half where each wave is left five K steps or more. Two blocks fit; asking
+// for two splits 448 in halves that take two rounds (200 rows, N 4096, K 4096: 21 against 17
+// us), asking for one leaves units with half their waves (40 rows of 16 experts, N 2816,
+// K 4096: 35 against 30), and four steps are too few to fill the ring (8 rows of 8 experts,
+// N 2816, K 4096, 4 parts instead of 8: the FFN 36.2 -> 34.9).
 inline int gemm_int8_splits(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int64_t mt = rows / kStreamRows + (rows < E ? rows : E);
+  const auto blocks = [&](int parts) { return mt * ((N * parts + kStreamCols - 1) / kStreamCols); };
   int parts = 1;
-  while (parts < 8 && K > 256 * parts && mt * ((N * parts + kStreamCols - 1) / kStreamCols) < 400)
+  while (parts < 8 && K > 256 * parts &&
+         (blocks(parts) < 256 || (blocks(parts) < 400 && K >= 1280 * parts)))
     parts *= 2;
   return parts;
 }
