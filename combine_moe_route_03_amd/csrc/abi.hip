@@ -764,13 +764,13 @@ int check_gemm_fp8_sizes(int64_t rows, int64_t E, int64_t N, int64_t K) {
   return MOE_OK;
 }
 
-// Rows of the norm and of the integer quantisation: 16-byte vectors counted in 32 bits,
-// a row in one block, grids of less than 2^32 threads.
-int check_row_sizes(int32_t dtype, int64_t rows, int64_t cols) {
+// Rows of the norm and of the integer quantisation: a row in one block, 16-byte vectors
+// and threads (up to 32 for each 128 columns) counted in 31 bits.
+int check_row_sizes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1) return MOE_ERR_ARG;
   if (cols % 16 != 0) return MOE_ERR_ALIGN;
   if (cols > moe::kMaxRow) return MOE_ERR_ARG;
-  if (rows * (dtype == MOE_BF16 ? 16 : 32) * ceil_div(cols, 128) >= kIndexLimit) return MOE_ERR_ARG;
+  if (rows * 32 * ceil_div(cols, 128) >= kIndexLimit) return MOE_ERR_ARG;
   return MOE_OK;
 }
 
@@ -786,7 +786,10 @@ int check_gemm_int8_sizes(int64_t rows, int64_t E, int64_t N, int64_t K, const i
     return MOE_ERR_ARG;
   const int64_t mtiles = rows / moe::kStreamRows + (rows < E ? rows : E);
   if (mtiles * ceil_div(N, 128) >= (int64_t(1) << 30)) return MOE_ERR_ARG;
-  if (mtiles * ceil_div(N, 32) >= (int64_t(1) << 32) / moe::kStreamThreads - 64)
+  // the streamed kernel has a block for each tile, in a grid of less than 2^32 threads
+  if (moe::gemm_int8_streams(rows, E, N, K) &&
+      mtiles * ceil_div(N * moe::gemm_int8_splits(rows, E, N, K), moe::kStreamCols) >=
+          (int64_t(1) << 32) / moe::kStreamThreads - 64)
     return MOE_ERR_ARG;
   return MOE_OK;
 }
@@ -899,7 +902,7 @@ int moe_expert_swiglu_fp8(const moe_shape* shape, int32_t I, const void* send_q,
 int moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32_t cols, void* q,
                       float* scale, moe_stream_t stream) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  const int st = check_row_sizes(dtype, rows, cols);
+  const int st = check_row_sizes(rows, cols);
   if (st != MOE_OK) return st;
   if (rows > 0 && (!x || !q || !scale)) return MOE_ERR_ARG;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_ALIGN;
@@ -911,7 +914,7 @@ int moe_add_rms_norm(int32_t dtype, int32_t q_dtype, int32_t T, int32_t H, const
                      void* q, float* scale, moe_stream_t stream) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (q && q_dtype != MOE_I8 && q_dtype != MOE_F8E4M3) return MOE_ERR_UNSUPPORTED;
-  const int st = check_row_sizes(dtype, T, H);
+  const int st = check_row_sizes(T, H);
   if (st != MOE_OK) return st;
   if (!(eps >= 0.0) || std::isinf(eps)) return MOE_ERR_ARG;
   if (!weight || (T > 0 && !x) || (q && !scale)) return MOE_ERR_ARG;

@@ -405,9 +405,9 @@ int moe_expert_swiglu_fp8(const moe_shape* shape, int32_t I, const void* send_q,
  * fp32 (at least 2^-126; 1 when amax is 0), q = the integer nearest to x / scale (the
  * exact quotient; ties to even). Infinities saturate to +-127; a row with a NaN has scale
  * NaN and q 0. Tokens are rows; so are the channels of weights [E][N][K], with rows = E * N.
- * cols % 16 == 0, cols <= 65536; rows * ceil(cols/128) < 2^27 for bf16, 2^26 for fp32;
- * x and q 16-byte aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also
- * cols % 16), MOE_ERR_UNSUPPORTED (dtype), MOE_ERR_DEVICE. */
+ * cols % 16 == 0, cols <= 65536; rows * ceil(cols/128) < 2^26; x and q 16-byte
+ * aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also cols % 16),
+ * MOE_ERR_UNSUPPORTED (dtype), MOE_ERR_DEVICE. */
 int moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32_t cols, void* q,
                       float* scale, moe_stream_t stream);
 
@@ -423,7 +423,7 @@ int moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32_t cols, 
  * x, residual, total, y [T][H] and weight [H] all of `dtype` (MOE_F32 or MOE_BF16). total
  * and y may each be the buffer of x or of the residual (not both the same one); no other
  * buffers may overlap. 0 <= eps < infinity; H % 16 == 0, H <= 65536, T * ceil(H/128) <
- * 2^27 for bf16, 2^26 for fp32; scale 4-byte, all others 16-byte aligned. One launch.
+ * 2^26; scale 4-byte, all others 16-byte aligned. One launch.
  * Errors: MOE_ERR_ARG (also a residual without total or total without one, or none of
  * total, y and q), MOE_ERR_ALIGN (also H % 16), MOE_ERR_UNSUPPORTED (dtype, or q_dtype with a q),
  * MOE_ERR_DEVICE. */
@@ -443,8 +443,8 @@ int moe_add_rms_norm(int32_t dtype, int32_t q_dtype, int32_t T, int32_t H, const
  * a [a_rows][K] int8 (a_rows == rows without row_token), a_scale [a_rows], w [E][N][K] int8,
  * w_scale [E][N], out [rows][N]. K % 16 == 0, K < 2^17, N % 16 == 0, 1 <= E <= 1024,
  * N*K < 2^31, 512*N < 2^30, E*N*K < 2^40, with row_token a_rows*K < 2^31, fewer than 2^30
- * tiles of 32 rows (+ min(rows, E)) by 128 columns, with at most 28 * E rows fewer than 2^23 - 64
- * by 32; a, w, w_scale, out 16-byte aligned.
+ * tiles of 32 rows (+ min(rows, E)) by 128 columns, with K <= 128 or at most 28 * E rows
+ * fewer than 2^23 - 64 by 256; a, w, w_scale, out 16-byte aligned.
  * One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED (out_dtype),
  * MOE_ERR_DEVICE. */
 int moe_expert_gemm_int8(int32_t rows, int32_t E, int32_t N, int32_t K, const void* a,

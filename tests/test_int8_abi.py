@@ -27,7 +27,8 @@ def test_reference_int8_rows():
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), UNSUPPORTED), (dict(dtype=3), UNSUPPORTED), (dict(rows=-1), ARG),
     (dict(cols=0), ARG), (dict(cols=24), ALIGN), (dict(cols=65552), ARG), (dict(rows=1 << 27), ARG),
-    (dict(rows=1 << 26, dtype=0), ARG), (dict(rows=1 << 26, cols=256), ARG), (dict(x=None), ARG),
+    (dict(rows=1 << 26, dtype=0), ARG), (dict(rows=1 << 26), ARG), (dict(rows=1 << 25, cols=144), ARG),
+    (dict(x=None), ARG),
     (dict(q=None), ARG), (dict(scale=None), ARG), (dict(x=ODD16), ALIGN), (dict(q=ODD16), ALIGN),
     (dict(scale=ODD4), ALIGN)])
 def test_quantize_int8_refusals(kw, status):
@@ -39,7 +40,7 @@ def test_quantize_int8_refusals(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), UNSUPPORTED), (dict(dtype=3), UNSUPPORTED), (dict(q_dtype=1), UNSUPPORTED),
     (dict(q_dtype=-1), UNSUPPORTED), (dict(T=-1), ARG), (dict(H=0), ARG), (dict(H=24), ALIGN),
-    (dict(H=65552), ARG), (dict(T=1 << 27), ARG), (dict(T=1 << 26, dtype=0), ARG),
+    (dict(H=65552), ARG), (dict(T=1 << 26), ARG), (dict(T=1 << 25, dtype=0, H=144), ARG),
     (dict(eps=-1e-6), ARG), (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG),
     (dict(x=None), ARG), (dict(weight=None), ARG), (dict(residual=None), ARG),
     (dict(total=None), ARG), (dict(scale=None), ARG), (dict(total=FAKE, y=FAKE), ARG),
@@ -81,8 +82,10 @@ def test_expert_gemm_int8_refusals(kw, status):
 
 
 def test_sizes_beyond_a_grid_are_refused():
-    args = (FAKE, FAKE, None, 1 << 28, FAKE, FAKE, FAKE, FAKE, 1, FAKE, None)
-    assert moe.lib().moe_expert_gemm_int8(1 << 28, 1, 256, 128, *args) == ARG
+    """A block of 512 threads for each tile of the streamed kernel; the tile list in 30 bits."""
+    for rows, N, K in ((1 << 28, 256, 128), (1 << 24, 4096, 112), (1 << 30, 4096, 4096)):
+        args = (FAKE, FAKE, None, rows, FAKE, FAKE, FAKE, FAKE, 1, FAKE, None)
+        assert moe.lib().moe_expert_gemm_int8(rows, 1, N, K, *args) == ARG
 
 
 def test_expert_swiglu_int8_refusals():
