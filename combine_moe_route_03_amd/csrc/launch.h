@@ -284,13 +284,18 @@ hipError_t launch_gemm_int8(const Int8Rows& a, int64_t rows, int E, const int32_
                             const int32_t* cnts, const void* w, const float* wsc, int N, int K,
                             int out_dtype, void* out, hipStream_t s);
 // Whether that product (or the gate/up product) streams the weights in 32-row tiles: few
-// rows an expert, bound by the weights' bytes either way; or few results in all, where the
-// tiled kernel is bound by the latency of its K steps, 19 us for K 4096 however few they
-// are (N 4096, one expert: 64 rows 9.6 against 19 us, 128 rows 12, 256 rows 17, 384 rows
-// 26). One K step is too short for the tiled kernel's stream of loads.
+// rows an expert on average, bound by the weights' bytes either way; or few results in all,
+// where the tiled kernel is bound by the latency of its K steps, 19 us for K 4096 however few
+// they are (N 4096, one expert: 64 rows 9.6 against 19 us, 128 rows 12, 256 rows 17, 384
+// rows 26). The tiled kernel gains with fewer steps a tile, since it reads a weight once for
+// all rows: 128 experts, even routing, streamed against tiled: K 4096, N 2816: 16 rows 252 and
+// 278 us, 28 rows 290 and 290; K 1408, N 4096: 8 rows 122 and 131, 12 rows 134 and 134, 28
+// rows 158 and 139; K 2816: 16 rows 262 and 256. One K step is too short for its stream of
+// loads.
 inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int64_t padded = rows + 16 * (rows < E ? rows : E);  // the tiles' rows, on average
-  return K <= 128 || rows <= kFewRows * E || padded * N <= (int64_t(1) << 20) + 16 * N;
+  return K <= 128 || rows <= (K < 4096 ? 14 : 28) * E ||
+         padded * N <= (int64_t(1) << 20) + 16 * N;
 }
 // The waves that share one group of weight rows in the streamed kernel, each a part of K
 // (a tile: kStreamRows rows by kStreamCols / parts): as many as give every compute unit a

@@ -82,14 +82,14 @@ def test_gemm_no_tokens(rows, K):
     assert (out == 0).all()
 
 
-# more than 28 rows an expert and 2^20 results: the tiled kernel, tiles of 1 to 256 rows;
+# more than 14 or 28 rows an expert and 2^20 results: the tiled kernel, tiles of 1 to 256 rows;
 # of up to 128 where there are few tiles or rows an expert and more than two K steps
 TILED = [[700], [255, 256, 257, 64, 65, 128, 129, 1, 0, 300], [1, 1999, 0], [513, 30, 31, 32, 33, 511],
-         [2047, 1, 897, 95, 0, 160], [33] * 40 + [127, 0, 31, 3]]
+         [2047, 1, 897, 95, 0, 160], [33] * 40 + [127, 0, 31, 3], [16, 0, 33, 1, 17, 96, 5, 18] * 8]
 
 
 def tiled(rows, E, N, K):
-    return K > 128 and rows > 28 * E and (rows + 16 * min(rows, E)) * N > 2 ** 20 + 16 * N
+    return K > 128 and rows > (14 if K < 4096 else 28) * E and (rows + 16 * min(rows, E)) * N > 2 ** 20 + 16 * N
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
