@@ -34,8 +34,7 @@ enum class Out { kBF16, kF32, kGateUp };
 // weights), and the K steps of its tiles are one stream: the loads run NS steps
 // ahead, into the next tile's first steps while this one's last run and its results are
 // stored. The tiles of an XCD's last, partial round are cut into two or four by
-// rows where that still gives each unit one, and come first: blocks then end their
-// tiles, and store, at different times.
+// rows where that still gives each unit one.
 //
 // Two shapes. 256 x 256, two stages: the fewest loads a product, for many rows. The K loop
 // runs at 2.5-2.8 POP/s, the matrix pipes 71% busy, and the clock falls from 2.4 to 1.9 GHz
@@ -87,16 +86,23 @@ __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
   const int whole = mine > 0 ? mine / hop * hop : 0, rest = mine - whole;
   const int cut = rest * 4 <= hop ? 4 : (rest * 2 <= hop ? 2 : 1);
   int place = blockIdx.x / kXCD;
-  const bool begins = place < rest * cut;  // with a part of a tile; then the whole rounds
-  const int limit = begins ? whole + hop : whole;
+  // Parts first: blocks then end their tiles, and store, at different times. Not long parts
+  // ahead of two rounds or more: the first loads of all blocks come from HBM at one time, and
+  // a part waits for them step by step (16384 rows of 16 experts, N 2816, K 4096: 207 us,
+  // 198 with them last; 24558 rows of 64, N 2048, K 1408: 105 and 108; 4096 rows of 4, N and
+  // K 4096: 77 and 80).
+  const bool early = KB < 16 || whole < 2 * hop;
+  const bool parts = place < rest * cut;
+  const int limit = parts ? whole + hop : whole;
   if (mine <= 0 || place >= limit) return;  // uniform over the block
   const auto tile_of = [&](int p) {
     if (p >= limit) return Tile{-1, 0, 0, 0};
-    const bool part = begins && p < hop;
+    const bool part = parts && (early ? p < hop : p >= whole);
+    const int q = part && !early ? p - whole : p;  // of the parts
     Tile t = tile_at_place<BM>(pre, offs, cnts, E, ntiles,
-                               first + (part ? whole + p / cut : begins ? p - hop : p));
+                               first + (part ? whole + q / cut : parts && early ? p - hop : p));
     if (part && cut > 1) {
-      const int r0 = p % cut * (BM / cut), left = t.rows - r0;
+      const int r0 = q % cut * (BM / cut), left = t.rows - r0;
       t.rows = left < BM / cut ? left : BM / cut;
       t.row0 += r0;
       if (left <= 0) t = {-1, 0, 0, 0};

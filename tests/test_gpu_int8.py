@@ -122,7 +122,8 @@ def test_gemm_tiled_no_tokens(rows):
 def test_gemm_tiled_rounds():
     """More tiles than compute units, with a rest that is cut; rows of all sizes."""
     g = torch.Generator().manual_seed(1)
-    for E, N, K, most in ((70, 4096, 272, 300), (5, 8208, 400, 2500), (300, 2064, 144, 130)):
+    for E, N, K, most in ((70, 4096, 272, 300), (5, 8208, 400, 2500), (300, 2064, 144, 130),
+                          (6, 8208, 2064, 2500), (40, 4112, 2304, 400)):
         counts = torch.randint(0, most, (E,), generator=g).tolist()
         offs, cnts, rows = buckets(counts)
         assert tiled(rows, E, N, K)
