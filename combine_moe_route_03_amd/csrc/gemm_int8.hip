@@ -535,6 +535,8 @@ hipError_t launch_expert_swiglu_int8(const Int8Rows& a, int64_t rows, int H, int
   if (rows == 0) return hipSuccess;
   hipError_t err = gemm(Out::kGateUp, a, rows, E, offs, cnts, w_gate_up, gsc, 2 * I, H, h, s);
   if (err != hipSuccess) return err;
+  if (rows <= kInnerRows && I <= kInnerCols)  // the second product makes them integers
+    return launch_gemm_int8_inner(h, rows, E, offs, cnts, w_down, dsc, H, I, out, s);
   err = launch_quantize_int8(h, MOE_F32, rows, I, hq, hs, s);
   if (err != hipSuccess) return err;
   return gemm(Out::kBF16, {hq, hs, nullptr, rows}, rows, E, offs, cnts, w_down, dsc, H, I, out, s);

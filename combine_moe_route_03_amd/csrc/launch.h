@@ -317,6 +317,12 @@ inline int gemm_int8_splits(int64_t rows, int64_t E, int64_t N, int64_t K) {
 hipError_t launch_gemm_int8_stream(bool gate_up, bool f32_out, const Int8Rows& a, int64_t rows,
                                    int E, const int32_t* offs, const int32_t* cnts, const void* w,
                                    const float* wsc, int N, int K, void* c, hipStream_t s);
+// out = the product of fp32 rows h, made integers as by quantize_int8, in bf16: up to
+// kInnerRows rows of kInnerCols columns.
+constexpr int kInnerRows = 8, kInnerCols = 2048;
+hipError_t launch_gemm_int8_inner(const float* h, int64_t rows, int E, const int32_t* offs,
+                                  const int32_t* cnts, const void* w, const float* wsc, int N, int K,
+                                  void* out, hipStream_t s);
 // The SwiGLU FFN on int8 rows: gate/up product with h = SiLU(g) u into h [rows][I] fp32,
 // its rows to hq and hs, the down product.
 hipError_t launch_expert_swiglu_int8(const Int8Rows& a, int64_t rows, int H, int I, int E,

@@ -282,11 +282,8 @@ __global__ __launch_bounds__(G ? kPackThreads : 1024) void quantize_int8_kernel(
       all = u > all ? u : all;
     }
   const Two<uint32_t, uint32_t> row = row_reduce<G>(all, top, tops, Max(), Max());
-  const bool nan = row.a > kInfBits;
-  const float s = int8_scale((double)__uint_as_float(row.b));
-  const float most = fminf(127.0f * s, 3.4028234663852886e38f);
-  const double inv = nan ? 0.0 : 1.0 / (double)s;
-  if (live && at.lane == 0) scale[at.row] = nan ? __builtin_nanf("") : s;
+  const Int8Row how = int8_row(row.a, row.b);
+  if (live && at.lane == 0) scale[at.row] = how.scale;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     const uint32_t c = j * at.lanes + at.lane;
@@ -295,8 +292,7 @@ __global__ __launch_bounds__(G ? kPackThreads : 1024) void quantize_int8_kernel(
     for (int i = 0; i < N / 4; ++i) {
       int b[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        b[k] = int8_round_exact(__builtin_amdgcn_fmed3f(t[j].get(4 * i + k), -most, most), inv);
+      for (int k = 0; k < 4; ++k) b[k] = how.round(t[j].get(4 * i + k));
       o[i] = pack_int8(b[0], b[1], b[2], b[3]);
     }
     if (live && c < nvec) put_q<kCache>(q + (base + c) * N, o);

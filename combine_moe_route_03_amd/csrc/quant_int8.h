@@ -32,6 +32,23 @@ __device__ __forceinline__ int int8_round_exact(float v, double inv) {
   return (int)(uint32_t)__double_as_longlong(fine + (kWhole - kFine));
 }
 
+// How an fp32 row is rounded. all, top: the largest magnitude (as bits) of its values and of
+// its finite ones.
+struct Int8Row {
+  float scale;  // NaN: of a row with one
+  float most;   // of a value's magnitude
+  double inv;
+  __device__ __forceinline__ int round(float v) const {
+    return int8_round_exact(__builtin_amdgcn_fmed3f(v, -most, most), inv);
+  }
+};
+__device__ __forceinline__ Int8Row int8_row(uint32_t all, uint32_t top) {
+  const bool nan = all > kInfBits;
+  const float s = int8_scale((double)__uint_as_float(top));
+  return {nan ? __builtin_nanf("") : s, fminf(127.0f * s, 3.4028234663852886e38f),
+          nan ? 0.0 : 1.0 / (double)s};
+}
+
 // Four integers in [-127, 127] as bytes.
 __device__ __forceinline__ uint32_t pack_int8(int a, int b, int c, int d) {
   const uint32_t lo = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0C0C0400u);

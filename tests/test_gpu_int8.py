@@ -265,6 +265,29 @@ def test_swiglu(T, H, E, k, I):
     assert torch.equal(rows, out)
 
 
+@pytest.mark.parametrize("H,E,k,I", [(272, 1, 1, 16), (144, 1, 1, 2048), (256, 1, 1, 2064),
+                                     (2064, 3, 2, 1408), (128, 40, 8, 400), (512, 2, 1, 272)])
+def test_swiglu_few_rows(H, E, k, I):
+    """A few rows by themselves and among many: the same bits, whoever makes the inner rows
+    integers; a NaN and inner rows past the range of fp32 among them."""
+    shape, d, idx, _, x, sx, wg, sg, wd, sd = ffn_case(40, H, E, k, I, seed=6)
+    sx = sx.clone()
+    sx[2], sx[3] = float("nan"), 1e30
+    many = moe.expert_swiglu_int8(x, sx, d["expert_offsets"], d["expert_counts"], shape, wg, sg, wd, sd,
+                                  row_token=d["row_token"])
+    for T in {1, 2, 3, 4, 5, 7, 8, 9} if k == 1 else {1, 8 // k, 8 // k + 1}:
+        print(f"[few rows] H={H} E={E} k={k} I={I} T={T}", flush=True)
+        few = moe.Shape(T, H, E, k, 1, 1, torch.bfloat16)
+        b = moe.alloc_dispatch(few, DEV)
+        moe.dispatch_index(idx[:T].contiguous(), few, b)
+        out = moe.expert_swiglu_int8(x[:T], sx[:T], b["expert_offsets"], b["expert_counts"], few, wg, sg,
+                                     wd, sd, row_token=b["row_token"])
+        got, want = out[b["pos"].flatten().long()], many[d["pos"][:T].flatten().long()]
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
+        if T <= 2:
+            check_ffn(out, b, x, sx, wg, sg, wd, sd)
+
+
 def test_swiglu_large_gates():
     """Gates of hundreds, where SiLU is the gate or nothing, and of zeros."""
     shape, d, _, _, x, sx, wg, sg, wd, sd = ffn_case(50, 256, 3, 1, 128, seed=3)
