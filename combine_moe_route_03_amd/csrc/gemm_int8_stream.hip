@@ -25,6 +25,11 @@ constexpr int kRows = kStreamRows;  // rows of a tile
 constexpr int kWaves = kStreamThreads / kWave;
 constexpr int kStageBytes = 4096 + kRows * 128;  // a wave's LDS: a step's weights and tokens
 
+// Whether rows of K bytes from w on are whole 128-byte lines.
+bool whole_lines(const void* w, int K) {
+  return ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)K) & 127) == 0;
+}
+
 // Steps in flight: what fits 128 registers (four waves a SIMD).
 template <int NB>
 constexpr int kRing = NB == 4 ? 2 : 3;
@@ -98,7 +103,9 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
 // fragment so that a lane's four results are g, g, u, u of two neighbouring columns), C
 // = h in fp32. N: rows of one expert's B (2 I for gate/up). tokens: rows of A that idx
 // may name, or null and A's rows lie in expert order.
-template <bool kGateUp, int WK, bool kF32Out>
+// kLines: rows of B are whole lines (16 tokens, 8 of 128 experts, H 4080, I 1392: the FFN 328
+// -> 275 us with lines that are not whole kept for the next step).
+template <bool kGateUp, int WK, bool kF32Out, bool kLines>
 __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ Asc, const int32_t* __restrict__ idx,
     uint32_t tokens, const int32_t* __restrict__ offs, const int32_t* __restrict__ cnts, int E,
@@ -221,11 +228,14 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
       emit(j / NTL, j % NTL, v);
     }
   };
-  // the expert's other tiles read the same weights
+  // Weights stay in the caches where the expert's other tiles read them too, or the next K
+  // step takes the rest of a line; else they go past them (gate/up of 128 tokens, 128 experts,
+  // N 2816, K 4096: 222 -> 195 us).
+  const std::bool_constant<!kLines> shared;
   if (tile.len > kRows) pass(std::integral_constant<int, 4>{}, std::true_type{});
-  else if (rows <= 8) pass(std::integral_constant<int, 1>{}, std::false_type{});
-  else if (rows <= 16) pass(std::integral_constant<int, 2>{}, std::false_type{});
-  else pass(std::integral_constant<int, 4>{}, std::false_type{});
+  else if (rows <= 8) pass(std::integral_constant<int, 1>{}, shared);
+  else if (rows <= 16) pass(std::integral_constant<int, 2>{}, shared);
+  else pass(std::integral_constant<int, 4>{}, shared);
 }
 
 // The FFN's second product for a few rows, from the inner rows in fp32: up to kInnerRows
@@ -241,7 +251,8 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
 constexpr int kInnerStride = kInnerCols + 32;
 static_assert(kInnerCols == 4 * kWave * kWaves && kInnerRows == 8, "a vector a thread; one group of rows");
 
-template <int WK>
+// kLines: rows of B are whole lines, which then go past the caches.
+template <int WK, bool kLines>
 __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_inner_kernel(
     const float* __restrict__ h, const int32_t* __restrict__ offs, const int32_t* __restrict__ cnts,
     int E, int64_t rows_total, const uint8_t* __restrict__ B, const float* __restrict__ Bsc, int N,
@@ -289,7 +300,8 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_inner_kernel(
   const auto load = [&](int u, int q) __attribute__((always_inline)) {
     const uint32_t at = (uint32_t)step_of(q) * 128;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) w[u][r] = load16_stream(wb.at(q < n), woff[r], at);
+    for (int r = 0; r < 4; ++r)
+      w[u][r] = kLines ? load16_stream(wb.at(q < n), woff[r], at) : load16(wb.at(q < n), woff[r], at);
   };
   __builtin_amdgcn_sched_barrier(0);  // the rows, which are waited for first, come first
 #pragma unroll
@@ -386,8 +398,9 @@ hipError_t run(const Int8Rows& a, int64_t rows, int E, const int32_t* offs, cons
   const int cols = kGateUp ? N / 2 : N;
   constexpr int kNO = kWaves / WK * (kGateUp ? 16 : 32);
   const int ntiles = (cols + kNO - 1) / kNO;
-  return launch(gemm_int8_stream_kernel<kGateUp, WK, kF32Out>, dim3(blocks(rows, E, ntiles)),
-                dim3(kWave * kWaves), 0, s,
+  return launch(whole_lines(w, K) ? gemm_int8_stream_kernel<kGateUp, WK, kF32Out, true>
+                                  : gemm_int8_stream_kernel<kGateUp, WK, kF32Out, false>,
+                dim3(blocks(rows, E, ntiles)), dim3(kWave * kWaves), 0, s,
                 static_cast<const uint8_t*>(a.q), a.scale, a.index, (uint32_t)a.rows, offs, cnts, E,
                 rows, static_cast<const uint8_t*>(w), wsc, N, K, c, ntiles);
 }
@@ -421,9 +434,9 @@ hipError_t launch_gemm_int8_inner(const float* h, int64_t rows, int E, const int
   return by_splits(rows, E, N, K, [&](auto wk) {
     constexpr int WK = decltype(wk)::value, kNO = kWaves / WK * 32;
     const int ntiles = (N + kNO - 1) / kNO;
-    return launch(gemm_int8_inner_kernel<WK>, dim3(blocks(rows, E, ntiles)), dim3(kWave * kWaves), 0,
-                  s, h, offs, cnts, E, rows, static_cast<const uint8_t*>(w), wsc, N, K,
-                  static_cast<uint16_t*>(c), ntiles);
+    return launch(whole_lines(w, K) ? gemm_int8_inner_kernel<WK, true> : gemm_int8_inner_kernel<WK, false>,
+                  dim3(blocks(rows, E, ntiles)), dim3(kWave * kWaves), 0, s, h, offs, cnts, E, rows,
+                  static_cast<const uint8_t*>(w), wsc, N, K, static_cast<uint16_t*>(c), ntiles);
   });
 }
 

@@ -290,11 +290,13 @@ hipError_t launch_gemm_int8(const Int8Rows& a, int64_t rows, int E, const int32_
 // rows 26). The tiled kernel gains with fewer steps a tile, since it reads a weight once for
 // all rows: 128 experts, even routing, streamed against tiled: K 4096, N 2816: 16 rows 252 and
 // 278 us, 28 rows 290 and 290; K 1408, N 4096: 8 rows 122 and 131, 12 rows 134 and 134, 28
-// rows 158 and 139; K 2816: 16 rows 262 and 256. One K step is too short for its stream of
-// loads.
+// rows 158 and 139; K 2816: 16 rows 262 and 256. Rows of weights that are no whole lines gain
+// earlier, their lines being cut at every step (100 experts: K 4112, N 2816: 6 rows 237 and
+// 240, 10 rows 250 and 243, 22 rows 294 and 251; K 1392, N 4096: 6 rows 122 and 126, 10 rows
+// 130 and 127). One K step is too short for its stream of loads.
 inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int64_t padded = rows + 16 * (rows < E ? rows : E);  // the tiles' rows, on average
-  return K <= 128 || rows <= (K < 4096 ? 14 : 28) * E ||
+  return K <= 128 || rows <= (K % 128 ? 8 : K < 4096 ? 14 : 28) * E ||
          padded * N <= (int64_t(1) << 20) + 16 * N;
 }
 // The waves that share one group of weight rows in the streamed kernel, each a part of K

@@ -89,7 +89,7 @@ TILED = [[700], [255, 256, 257, 64, 65, 128, 129, 1, 0, 300], [1, 1999, 0], [513
 
 
 def tiled(rows, E, N, K):
-    return K > 128 and rows > (14 if K < 4096 else 28) * E and (rows + 16 * min(rows, E)) * N > 2 ** 20 + 16 * N
+    return K > 128 and rows > (8 if K % 128 else 14 if K < 4096 else 28) * E and (rows + 16 * min(rows, E)) * N > 2 ** 20 + 16 * N
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -286,6 +286,17 @@ def test_swiglu_few_rows(H, E, k, I):
         assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
         if T <= 2:
             check_ffn(out, b, x, sx, wg, sg, wd, sd)
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 256, 128), (40, 256, 384), (40, 272, 144), (300, 512, 640)])
+def test_swiglu_weights_off_a_line(T, H, I):
+    """Weights that begin 16 bytes past a line give the bits of those that begin on one."""
+    shape, d, _, _, x, sx, wg, sg, wd, sd = ffn_case(T, H, 4, 2, I, seed=7)
+    off = lambda w: torch.cat([w.new_zeros(16), w.flatten()])[16:].view(w.shape)
+    args = d["expert_offsets"], d["expert_counts"], shape
+    want = moe.expert_swiglu_int8(x, sx, *args, wg, sg, wd, sd, row_token=d["row_token"])
+    assert torch.equal(moe.expert_swiglu_int8(x, sx, *args, off(wg), sg, off(wd), sd,
+                                              row_token=d["row_token"]), want)
 
 
 def test_swiglu_large_gates():
