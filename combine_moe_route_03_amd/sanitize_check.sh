@@ -23,4 +23,4 @@ export MOE_ROUTE_LIB=$OUT/libmoe_route_san.so
 export LD_PRELOAD=$(ls /opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so | head -1)
 export ASAN_OPTIONS=detect_leaks=0:abort_on_error=1
 export UBSAN_OPTIONS=halt_on_error=1:print_stacktrace=1
-python3 -m pytest tests/test_abi.py tests/test_fp8_abi.py tests/test_fp8_limits.py -q -p no:cacheprovider "$@"
+python3 -m pytest tests/test_abi.py tests/test_fp8_abi.py tests/test_fp8_limits.py tests/test_int8_abi.py -q -p no:cacheprovider "$@"
