@@ -36,14 +36,14 @@ enum class Out { kBF16, kF32, kGateUp };
 // stored. The tiles of an XCD's last, partial round are cut into two or four by
 // rows where that still gives each unit one.
 //
-// Two shapes. 256 x 256, two stages: the fewest loads a product, for many rows. The K loop
-// runs at 2.5-2.8 POP/s, the matrix pipes 71% busy, and the clock falls from 2.4 to 1.9 GHz
-// under it: power bounds it, so what saves energy counts (the 32 x 32 x 32 instruction,
-// with twice the sums' traffic a product, ran at 1.7 GHz: 213 against 187 us for 8192 x
-// 4096 x 7168; 4 waves of 128 x 128 spill: 222). 128 x 256, three stages: twice the time for
-// a load to land, for few tiles, whose steps are as long as a load takes (0.95 us with two
-// stages, 0.5 with three: 1024 x 4096 x 4096 32 against 23 us), and for short experts; with
-// many rows its 1.5 times the loads cost more than it gains (8192 rows 212 against 190 us).
+// Two shapes. 256 x 256, two stages: the fewest loads a product, for many rows. 8192 x 4096 x
+// 7168 take 177-180 us, 2.7 POP/s; in the K loop the matrix pipes are 71% busy, and the clock
+// falls from 2.4 to 1.9 GHz under it: power bounds it, so what saves energy counts (the
+// 32 x 32 x 32 instruction, with twice the sums' traffic a product, ran at 1.7 GHz: 213 us;
+// 4 waves of 128 x 128 spill: 222). 128 x 256, three stages: twice the time for a load to land,
+// for few tiles, whose steps are as long as a load takes (0.95 us with two stages, 0.5 with
+// three: 1024 x 4096 x 4096 32 against 23 us), and for short experts; with many rows its 1.5
+// times the loads cost more than it gains (the 8192 rows 212 us).
 template <Out kOut, bool kGather, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(kWave * WM * WN, 1) void gemm_int8_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ Asc, const int32_t* __restrict__ idx,

@@ -8,7 +8,9 @@
 //
 // A wave computes 32 weight rows by up to 32 tokens, K steps of 128 bytes. With one
 // scale a row and a column the sums need no step of their own: the matrix instruction
-// adds them up through the whole of K.
+// adds them up through the whole of K. 1024 rows of 128 experts, N 2816, K 4096: 194 us, 6.4
+// TB/s; 5 rows of one, N 4096, K 7168: 10 us, of which a product of next to nothing takes
+// 5.4 (launch, tile, first loads, the join).
 #include <type_traits>
 
 #include "device.h"

@@ -9,7 +9,9 @@
 // border between two integers lands on its own side.
 //
 // Bound by HBM bytes: every element is read once and kept in registers between the
-// row's reduction and the outputs.
+// row's reduction and the outputs. Norm of 16384 x 7168 bf16 with the residual, y and int8 rows
+// out: 172 us, 6.1 TB/s; 45056 x 4096 bf16 to int8: 86 us, 6.4 TB/s. One row of 4096: 3.4 us
+// in a graph, latency.
 #include <type_traits>
 
 #include "device.h"
@@ -302,10 +304,10 @@ __global__ __launch_bounds__(G ? kPackThreads : 1024) void quantize_int8_kernel(
 // Lanes and vectors a lane of a row: f(G, P, block, rows a block). Many rows take a wave
 // each, up to eight vectors a lane, or else blocks of four vectors a lane: with a vector a
 // lane, and so a block of many waves a row, the barriers of the reduction leave the memory
-// idle (45056 rows of 4096 bf16 to int8 151 against 96 us; norm of 16384 rows of 7168 207
-// against 178). Few rows take as many lanes as they have vectors, since they are bound
-// by latency, but for more than 512 lanes, which take longer to begin (1 row of 7168 5.1
-// against 4.3 us, 512 rows 11 against 9).
+// idle (when that was measured, 45056 rows of 4096 bf16 to int8 151 against 96 us, norm of
+// 16384 rows of 7168 207 against 178). Few rows take as many lanes as they have vectors,
+// since they are bound by latency, but for more than 512 lanes, which take longer to begin
+// (1 row of 7168 5.1 against 4.3 us, 512 rows 11 against 9).
 template <bool kBF16, typename F>
 hipError_t by_row(uint32_t rows, uint32_t nvec, const F& f) {
   constexpr int kPart = kBF16 ? 16 : 32;  // lanes of 128 columns

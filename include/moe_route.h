@@ -406,7 +406,7 @@ int moe_expert_swiglu_fp8(const moe_shape* shape, int32_t I, const void* send_q,
  * exact quotient; ties to even). Infinities saturate to +-127; a row with a NaN has scale
  * NaN and q 0. Tokens are rows; so are the channels of weights [E][N][K], with rows = E * N.
  * cols % 16 == 0, cols <= 65536; rows * ceil(cols/128) < 2^26; x and q 16-byte
- * aligned. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also cols % 16),
+ * aligned, no two buffers overlap. One launch. Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (also cols % 16),
  * MOE_ERR_UNSUPPORTED (dtype), MOE_ERR_DEVICE. */
 int moe_quantize_int8(const void* x, int32_t dtype, int32_t rows, int32_t cols, void* q,
                       float* scale, moe_stream_t stream);
@@ -467,7 +467,7 @@ size_t moe_expert_swiglu_int8_workspace_bytes(const moe_shape* shape, int32_t I)
  * [E][H], expert_out [T*k][H] bf16. H % 16 == 0, I % 16 == 0, I <= 65536,
  * T * k * ceil(I/128) < 2^26 and the limits of moe_expert_gemm_int8 for both products. workspace:
  * moe_expert_swiglu_int8_workspace_bytes(shape, I) bytes, 16-byte aligned, clobbered; calls
- * that overlap need one each. Three launches.
+ * that overlap need one each. Three launches; two for up to 8 rows with I <= 2048.
  * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_UNSUPPORTED,
  *         MOE_ERR_DEVICE. */
 int moe_expert_swiglu_int8(const moe_shape* shape, int32_t I, const void* x_q,
