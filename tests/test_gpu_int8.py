@@ -338,6 +338,24 @@ def test_swiglu_leaves_other_rows():
     check_ffn(out, d, x, sx, wg, sg, wd, sd)
 
 
+def test_swiglu_few_rows_in_buckets():
+    """Buckets of a few rows: with gaps, out of order, past the rows, and none."""
+    shape, d, _, _, x, sx, wg, sg, wd, sd = ffn_case(8, 272, 4, 1, 144, seed=5)
+    for offs, cnts in (([5, 0, 3, 8], [3, 2, 1, 1]), ([-1, 2, 7, 0], [3, 4, 2, 0]), ([0, 0, 0, 0], [0, 0, 0, 0]),
+                       ([0, 4, 2, 6], [1, 1, 1, 1]), ([0, 0, 0, 0], [0, 0, 9, 0]), ([4, 0, 0, 0], [-1, 0, 4, 0])):
+        live = [(e, o, n) for e, (o, n) in enumerate(zip(offs, cnts)) if o >= 0 and n > 0 and o + n <= 8]
+        ws = torch.full((moe.expert_swiglu_int8_workspace_bytes(shape, 144),), 0xFF, dtype=torch.uint8, device=DEV)
+        out = torch.full((8, 272), 9.0, dtype=torch.bfloat16, device=DEV)
+        moe.expert_swiglu_int8(x, sx, torch.tensor(offs, **I32), torch.tensor(cnts, **I32), shape, wg, sg, wd, sd,
+                               expert_out=out, workspace=ws)
+        rest = torch.ones(8, dtype=torch.bool, device=DEV)
+        for e, o, n in live:
+            rest[o:o + n] = False
+            y, bound = ref.swiglu(x[o:o + n], sx[o:o + n], wg[e], sg[e], wd[e], sd[e])
+            assert ((out[o:o + n].double() - y).abs() <= bound).all(), (offs, e)
+        assert (out[rest] == 9).all(), offs
+
+
 # ------------------------------------------------------------------- together
 
 def block_buffers(T, H, E, k, I, seed):
@@ -392,7 +410,7 @@ def test_block(T, H, E, k, I):
     check_block(b)
 
 
-@pytest.mark.parametrize("T,H,E,k,I", [(5, 512, 16, 4, 208), (700, 512, 8, 2, 256)])
+@pytest.mark.parametrize("T,H,E,k,I", [(2, 512, 16, 4, 208), (5, 512, 16, 4, 208), (700, 512, 8, 2, 256)])
 def test_block_captured(T, H, E, k, I):
     """Replayed with new inputs and eager calls on other buffers in between."""
     b, other = block_buffers(T, H, E, k, I, seed=7), block_buffers(T, H, E, k, I, seed=8)
