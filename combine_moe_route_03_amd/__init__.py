@@ -817,13 +817,21 @@ def expert_swiglu_fp8(send_q: torch.Tensor, send_scale: torch.Tensor,
 _Q_CODE = {torch.int8: MOE_I8, _FP8: MOE_F8E4M3}
 
 
-def _rows(shape: torch.Size) -> int:
-    """Rows of a tensor of this shape; they and the columns fit 32 bits."""
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    _int32(rows, shape[-1])
+def _rows(x: torch.Tensor, cols: int) -> int:
+    """Rows of a tensor of so many columns; both fit 32 bits."""
+    rows = x.numel() // cols if cols else 0
+    if rows >= 1 << 31 or cols >= 1 << 31:
+        raise ValueError(f"sizes must fit 32 bits, got {(rows, cols)}")
     return rows
+
+
+def _stream_of(x: torch.Tensor) -> int:
+    """_current_stream of a tensor's device, without a look at the device's name (the calls
+    of one token take 3-4 us on the device)."""
+    index = x.get_device()  # -1: host memory
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current device, got {x.device}")
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
@@ -843,7 +851,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
     if not shape:
         raise ValueError("x needs at least one dimension")
     H = shape[-1]
-    rows = _rows(shape)
+    rows = _rows(x, H)
     at_t = at_r = at_y = at_q = at_s = None
     if residual is not None:
         total = _empty(shape, dt, dev) if total is None else total
@@ -874,7 +882,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
     _check(lib().moe_add_rms_norm(
         code, q_code, rows, H, _checked("x", x, shape, dt, dev), at_r,
         _checked("weight", weight, (H,), dt, dev), eps, at_t, at_y, at_q, at_s,
-        _current_stream(dev)), "moe_add_rms_norm")
+        _stream_of(x)), "moe_add_rms_norm")
     return total, y, q, scale
 
 
@@ -888,13 +896,13 @@ def quantize_int8(x: torch.Tensor, q: torch.Tensor | None = None,
         raise ValueError("x needs at least one dimension")
     dev, shape = x.device, x.shape
     cols = shape[-1]
-    rows = _rows(shape)
+    rows = _rows(x, cols)
     q = _empty(shape, torch.int8, dev) if q is None else q
     scale = _empty(shape[:-1], torch.float32, dev) if scale is None else scale
     _check(lib().moe_quantize_int8(
         _checked("x", x, shape, x.dtype, dev), _DTYPE_CODE[x.dtype], rows, cols,
         _checked("q", q, shape, torch.int8, dev),
-        _checked("scale", scale, shape[:-1], torch.float32, dev), _current_stream(dev)),
+        _checked("scale", scale, shape[:-1], torch.float32, dev), _stream_of(x)),
         "moe_quantize_int8")
     return q, scale
 
@@ -924,7 +932,7 @@ def expert_gemm_int8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: tor
         _checked("expert_offsets", expert_offsets, (E,), i32, dev),
         _checked("expert_counts", expert_counts, (E,), i32, dev), _checked("w", w, (E, N, K), i8, dev),
         _checked("w_scale", w_scale, (E, N), f32, dev), _DTYPE_CODE[out.dtype],
-        _checked("out", out, (rows, N), out.dtype, dev), _current_stream(dev)),
+        _checked("out", out, (rows, N), out.dtype, dev), _stream_of(a)),
         "moe_expert_gemm_int8")
     return out
 
@@ -966,7 +974,7 @@ def expert_swiglu_int8(x_q: torch.Tensor, x_scale: torch.Tensor, expert_offsets:
         _checked("s_down", s_down, (E, H), f32, dev),
         _checked("expert_out", expert_out, (rows, H), torch.bfloat16, dev),
         _checked("workspace", workspace, tuple(workspace.shape), torch.uint8, dev), workspace.numel(),
-        _current_stream(dev)), "moe_expert_swiglu_int8")
+        _stream_of(x_q)), "moe_expert_swiglu_int8")
     return expert_out
 
 

@@ -37,7 +37,7 @@ enum class Out { kBF16, kF32, kGateUp };
 // rows where that still gives each unit one.
 //
 // Two shapes. 256 x 256, two stages: the fewest loads a product, for many rows. 8192 x 4096 x
-// 7168 take 177-180 us, 2.7 POP/s; in the K loop the matrix pipes are 71% busy, and the clock
+// 7168 take 175-180 us, 2.7 POP/s; in the K loop the matrix pipes are 71% busy, and the clock
 // falls from 2.4 to 1.9 GHz under it: power bounds it, so what saves energy counts (the
 // 32 x 32 x 32 instruction, with twice the sums' traffic a product, ran at 1.7 GHz: 213 us;
 // 4 waves of 128 x 128 spill: 222). 128 x 256, three stages: twice the time for a load to land,
