@@ -9,7 +9,7 @@
 // A wave computes 32 weight rows by up to 32 tokens, K steps of 128 bytes. With one
 // scale a row and a column the sums need no step of their own: the matrix instruction
 // adds them up through the whole of K. 1024 rows of 128 experts, N 2816, K 4096: 194 us, 6.4
-// TB/s; 5 rows of one, N 4096, K 7168: 10 us, of which a product of next to nothing takes
+// TB/s; 5 rows of one, N 4096, K 7168: 8.9 us, of which a product of next to nothing takes
 // 5.4 (launch, tile, first loads, the join).
 #include <type_traits>
 
@@ -32,9 +32,10 @@ bool whole_lines(const void* w, int K) {
   return ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)K) & 127) == 0;
 }
 
-// Steps in flight: what fits 128 registers (four waves a SIMD).
-template <int NB>
-constexpr int kRing = NB == 4 ? 2 : 3;
+// Steps in flight of F fragments of 16 weight rows: what fits 128 registers (four waves a
+// SIMD).
+template <int NB, int F>
+constexpr int kRing = F == 1 ? (NB == 4 ? 3 : 5) : (NB == 4 ? 2 : 3);
 
 // acc[f][t] += products of weight fragment f (16 rows) with tokens 16 t .. 16 t + 15
 // over the K steps s0 .. s0 + n - 1, beginning with step s0 + rot. woff: byte offsets in
@@ -43,22 +44,22 @@ constexpr int kRing = NB == 4 ? 2 : 3;
 // last, keep: the step that holds the end of a row, and whether the lane's chunk of it is
 // in the row; past it the tokens are zeros, so it does not matter what the weights are.
 // kShared: other blocks read these weights.
-template <int NB, bool kShared>
+template <int NB, int F, bool kShared>
 __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
-                                          const uint32_t (&woff)[4], const int (&wrow)[2],
+                                          const uint32_t (&woff)[2 * F], const int (&wrow)[2],
                                           const Buffer& xb, const uint32_t (&xoff)[NB], int s0,
                                           int n, int rot, int last, bool keep,
-                                          i32x4 (&acc)[2][(NB + 1) / 2]) {
-  constexpr int NTL = (NB + 1) / 2, D = kRing<NB>;
+                                          i32x4 (&acc)[F][(NB + 1) / 2]) {
+  constexpr int NTL = (NB + 1) / 2, D = kRing<NB, F>;
   const int lane = threadIdx.x & (kWave - 1);
   const int lr = lane >> 3, lc = lane & 7, i = lane & 15, g = lane >> 4;
-  v4u w[D][4], x[D][NB];
+  v4u w[D][2 * F], x[D][NB];
   auto load = [&](int u, int q) __attribute__((always_inline)) {
     const bool in = q < n;
     const uint32_t s = in ? (uint32_t)(s0 + (q + rot >= n ? q + rot - n : q + rot)) : 0;
     const bool cut = (int)s == last && !keep;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 2 * F; ++r)
       w[u][r] = kShared ? load16(wb.at(in), woff[r], s * 128)
                         : load16_stream(wb.at(in), woff[r], s * 128);
 #pragma unroll
@@ -70,20 +71,22 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
   };
   auto compute = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 2 * F; ++r)
       *reinterpret_cast<v4u*>(stage + 2048 * (r >> 1) + tile_at(wrow[r & 1], lc)) = w[u][r];
 #pragma unroll
     for (int b = 0; b < NB; ++b) *reinterpret_cast<v4u*>(xs + tile_at(8 * b + lr, lc)) = x[u][b];
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // halves of the 128 bytes
-      const i32x4 a[2] = {frag(stage, i, g + 4 * h), frag(stage + 2048, i, g + 4 * h)};
+      i32x4 a[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f) a[f] = frag(stage + 2048 * f, i, g + 4 * h);
 #pragma unroll
       for (int t = 0; t < NTL; ++t) {
         // with one group of 8 tokens its rows twice (columns 8-15 unused)
         const i32x4 tok = frag(xs, NB == 1 ? i & 7 : 16 * t + i, g + 4 * h);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) acc[f][t] = mfma_int8(a[f], tok, acc[f][t]);
+        for (int f = 0; f < F; ++f) acc[f][t] = mfma_int8(a[f], tok, acc[f][t]);
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -107,14 +110,16 @@ __device__ __forceinline__ void dot_steps(uint8_t* stage, const Buffer& wb,
 // may name, or null and A's rows lie in expert order.
 // kLines: rows of B are whole lines (16 tokens, 8 of 128 experts, H 4080, I 1392: the FFN 328
 // -> 275 us with lines that are not whole kept for the next step).
-template <bool kGateUp, int WK, bool kF32Out, bool kLines>
+// F: fragments of 16 weight rows a wave, 2, or 1 where the columns are few (groups of 16).
+template <bool kGateUp, int WK, bool kF32Out, bool kLines, int F>
 __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ Asc, const int32_t* __restrict__ idx,
     uint32_t tokens, const int32_t* __restrict__ offs, const int32_t* __restrict__ cnts, int E,
     int64_t rows_total, const uint8_t* __restrict__ B, const float* __restrict__ Bsc, int N, int K,
     void* __restrict__ C, int ntiles) {
   constexpr int kGroups = kWaves / WK;
-  constexpr int kGroupCols = kGateUp ? 16 : 32;
+  constexpr int kGroupCols = kGateUp ? 16 : 16 * F;
+  static_assert(F == 2 || !kGateUp, "gate and up rows");
   constexpr int kNO = kGroups * kGroupCols;  // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][kStageBytes];
   __shared__ __attribute__((aligned(16))) float row_scale[kWave], col_scale[kStreamCols];
@@ -135,9 +140,9 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
   const Buffer xb = {idx ? A : A + (int64_t)row0 * K,
                      (idx ? (tokens ? tokens : 1) : (uint32_t)rows) * (uint32_t)K};
   const int n0 = tile.ntile * kNO + group * kGroupCols;  // the group's first column
-  uint32_t woff[4];
+  uint32_t woff[2 * F];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < 2 * F; ++r) {
     // gate/up: gate and up rows of 8 columns a fragment; plain: 8 rows each (those
     // past the last one, in the last tile, do not exist)
     const int c = kGateUp ? n0 + 8 * (r >> 1) + lr : n0 + 8 * r + lr;
@@ -153,7 +158,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
   };
   // The tile's scales go straight into LDS, where they are when the products are: rows of
   // w by waves 0 and up (gate/up: the gate rows, then the up rows), rows of A by the last.
-  constexpr int kWRows = kStreamCols / WK;
+  constexpr int kWRows = kGroups * 16 * F;
   if (wid * kWave < kWRows) {
     const int r = wid * kWave + lane, c = kGateUp && r >= kNO ? r - kNO : r;
     const int n = tile.ntile * kNO + c + (kGateUp && r >= kNO ? I : 0);
@@ -169,19 +174,19 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
   auto pass = [&](auto nb_, auto shared) __attribute__((always_inline)) {
     constexpr int NB = decltype(nb_)::value, NTL = (NB + 1) / 2;
     uint32_t xoff[NB];
-    i32x4 acc[2][NTL];
+    i32x4 acc[F][NTL];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const uint32_t m = 8 * b + lr, r = idx ? source(m) : m;
       xoff[b] = (int)m < rows && (!idx || r < tokens) ? r * (uint32_t)K + 16 * lc : kOutside;
     }
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int t = 0; t < NTL; ++t) acc[f][t] = i32x4{0, 0, 0, 0};
     const int s0 = KB * part / WK, n = KB * (part + 1) / WK - s0;
     if (n > 0)  // uniform over the wave
-      dot_steps<NB, decltype(shared)::value>(stage[wid], wb, woff, wrow, xb, xoff, s0, n,
+      dot_steps<NB, F, decltype(shared)::value>(stage[wid], wb, woff, wrow, xb, xoff, s0, n,
                                              (int)((uint32_t)(tile.ntile + row0) * 5 % (uint32_t)n), KB - 1,
                                              16 * lc < K - 128 * (KB - 1), acc);
     // lane l's results of fragments f and t: columns n0 + 16 f (8 f) + ..., token 16 t + i
@@ -214,7 +219,7 @@ __global__ __launch_bounds__(kWave * kWaves, 4) void gemm_int8_stream_kernel(
     };
     // Every wave's sums in its stage, of which the group's waves then take the fragments
     // in turn (also a wave alone: results straight from the registers made it spill).
-    constexpr int kFrags = 2 * NTL;
+    constexpr int kFrags = F * NTL;
     i32x4* own = reinterpret_cast<i32x4*>(stage[wid]);
     static_assert(kFrags * kWave * 16 <= kStageBytes, "sums fit the stage");
 #pragma unroll
@@ -394,14 +399,14 @@ unsigned blocks(int64_t rows, int E, int ntiles) {
   return (unsigned)(runs * kGroupM * kXCD);
 }
 
-template <bool kGateUp, int WK, bool kF32Out>
+template <bool kGateUp, int WK, bool kF32Out, int F = 2>
 hipError_t run(const Int8Rows& a, int64_t rows, int E, const int32_t* offs, const int32_t* cnts,
                const void* w, const float* wsc, int N, int K, void* c, hipStream_t s) {
   const int cols = kGateUp ? N / 2 : N;
-  constexpr int kNO = kWaves / WK * (kGateUp ? 16 : 32);
+  constexpr int kNO = kWaves / WK * (kGateUp ? 16 : 16 * F);
   const int ntiles = (cols + kNO - 1) / kNO;
-  return launch(whole_lines(w, K) ? gemm_int8_stream_kernel<kGateUp, WK, kF32Out, true>
-                                  : gemm_int8_stream_kernel<kGateUp, WK, kF32Out, false>,
+  return launch(whole_lines(w, K) ? gemm_int8_stream_kernel<kGateUp, WK, kF32Out, true, F>
+                                  : gemm_int8_stream_kernel<kGateUp, WK, kF32Out, false, F>,
                 dim3(blocks(rows, E, ntiles)), dim3(kWave * kWaves), 0, s,
                 static_cast<const uint8_t*>(a.q), a.scale, a.index, (uint32_t)a.rows, offs, cnts, E,
                 rows, static_cast<const uint8_t*>(w), wsc, N, K, c, ntiles);
@@ -425,6 +430,14 @@ hipError_t launch_gemm_int8_stream(bool gate_up, bool f32_out, const Int8Rows& a
   return by_splits(rows, E, N, K, [&](auto wk) {
     constexpr int WK = decltype(wk)::value;
     if (gate_up) return run<true, WK, true>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
+    // Half the units and more without a block: groups of 16 columns, the same bytes of
+    // weights in flight a wave (5 rows, N 4096, K 7168: 10.2 -> 8.9 us; 30 rows, N 2048: 12.6 ->
+    // 10.8; 1 row, K 14336: 15.1 -> 12.0; 64 rows, N 2048, K 7168: 10.4 and 10.5).
+    if constexpr (WK == kWaves) {
+      if ((rows / kRows + (rows < E ? rows : E)) * ((N + 31) / 32) <= 128)
+        return f32_out ? run<false, WK, true, 1>(a, rows, E, offs, cnts, w, wsc, N, K, c, s)
+                       : run<false, WK, false, 1>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
+    }
     return f32_out ? run<false, WK, true>(a, rows, E, offs, cnts, w, wsc, N, K, c, s)
                    : run<false, WK, false>(a, rows, E, offs, cnts, w, wsc, N, K, c, s);
   });

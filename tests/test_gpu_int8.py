@@ -110,6 +110,17 @@ def test_gemm_tiled(N, K, counts, dtype):
     check(ints(37, K, seed=6), scales(37, seed=7), offs, cnts, w, sw, index=index, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts", [[1], [5], [8], [9], [17], [32], [33], [1, 0, 2], [0, 40, 3, 8]], ids=str)
+@pytest.mark.parametrize("N,K", [(16, 1040), (48, 7168), (1040, 2064), (2064, 1536), (4112, 4096)])
+def test_gemm_few_columns(N, K, counts, dtype):
+    """Few tiles: every wave of a block a part of K, groups of 16 columns and of 32."""
+    offs, cnts, rows = buckets(counts)
+    E = len(counts)
+    check(ints(rows, K, seed=1), scales(rows, seed=2), offs, cnts, ints(E, N, K, seed=3),
+          scales(E, N, seed=4), dtype=dtype)
+
+
 @pytest.mark.parametrize("rows", [900, 4000])
 def test_gemm_tiled_no_tokens(rows):
     index = torch.zeros(rows, **I32)
