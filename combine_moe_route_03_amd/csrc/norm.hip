@@ -50,8 +50,9 @@ __device__ __forceinline__ v4u pack_row(const float (&f)[RowVec<kBF16>::N]) {
 // that of one rounding from 64 bits: where anything lies below the 11th bit, that bit is set and
 // the 10 below it are cleared, so that fp32 cannot round the rest onto the border between two
 // values. (From 2^-139 on 11 bits are whole steps of fp32; what is less is zero in bf16.) Four
-// instructions on the high word: the norm of 16384 x 7168 bf16, int8 rows out, 173 -> 174 us, 512
-// rows of 65536 77 -> 79 (with fp32 first and a branch for values on a border 83).
+// instructions on the high word: the norm of 16384 x 7168 bf16, int8 rows out, 173 -> 174 us, e4m3
+// rows 175 -> 176.5; 512 rows of 65536 77 -> 78 (with fp32 first and a branch for values on a
+// border 83).
 __device__ __forceinline__ float narrow(double v) {
   const uint64_t u = (uint64_t)__double_as_longlong(v);
   const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
@@ -225,10 +226,13 @@ __global__ __launch_bounds__(G ? kPackThreads : 1024) void add_rms_norm_kernel(
     double v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = (double)t[j].get(i) * (double)w[j].get(i) * r;
+    float n[N];  // for bf16 and e4m3
+#pragma unroll
+    for (int i = 0; i < N; ++i) n[i] = narrow(v[i]);
     if (y && ok) {
       float f[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = kBF16 ? narrow(v[i]) : (float)v[i];
+      for (int i = 0; i < N; ++i) f[i] = kBF16 ? n[i] : (float)v[i];
       put<kCache>(y + base + c, pack_row<kBF16>(f));
     }
     if constexpr (kQ == kInt8) {
@@ -253,12 +257,19 @@ __global__ __launch_bounds__(G ? kPackThreads : 1024) void add_rms_norm_kernel(
       }
       m = group_reduce(m, kGroup, Max());
       const int p = scale_exponent(m);
-      const double f = __longlong_as_double((long long)(1023 - p) << 52);  // 2^-p
+      float f = 1.0f;
+      if (__any(p > 118)) {  // y may be past the range of fp32
+        const double d = __longlong_as_double((long long)(1023 - p) << 52);  // 2^-p
+#pragma unroll
+        for (int i = 0; i < N; ++i) n[i] = narrow(v[i] * d);
+      } else {
+        f = power_of_two(-p);  // n 2^-p is exact, or too small for e4m3
+      }
       uint32_t o[N / 4];
 #pragma unroll
       for (int i = 0; i < N / 4; ++i)
-        o[i] = e4m3x4(e4m3_clamp((float)(v[4 * i] * f)), e4m3_clamp((float)(v[4 * i + 1] * f)),
-                      e4m3_clamp((float)(v[4 * i + 2] * f)), e4m3_clamp((float)(v[4 * i + 3] * f)));
+        o[i] = e4m3x4(e4m3_clamp(n[4 * i] * f), e4m3_clamp(n[4 * i + 1] * f),
+                      e4m3_clamp(n[4 * i + 2] * f), e4m3_clamp(n[4 * i + 3] * f));
       if (ok) {
         put_q<kCache>(q + (base + c) * N, o);
         const uint32_t groups = (nvec + kGroup - 1) / kGroup;

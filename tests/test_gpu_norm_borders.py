@@ -1,5 +1,5 @@
 """The norm's rows next to the border between two values of their type: one rounding from
-the 64-bit y to bf16.
+the 64-bit y to bf16, and one to e4m3.
 
 Every y is m (1 + d), m half way between two neighbours, with |d| far below a step of fp32:
 t w = 3 m from two factors of few bits, and eps makes the row's factor (1 + d) / 3. What the
@@ -12,7 +12,7 @@ import combine_moe_route_03_amd as moe
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
-BF16 = torch.bfloat16
+BF16, F32 = torch.bfloat16, torch.float32
 OFFS = [s * 2.0 ** -p for p in (27, 33, 40) for s in (1, -1)]
 
 
@@ -63,5 +63,35 @@ def test_bf16(where, T, H):
         got = norm(t, w, off, T, BF16)[1].double().cpu()
         want = m + m.sign() * (unit if off > 0 else -unit)
         want[want.abs() >= 2.0 ** 128] *= float("inf")
+        bad = (got != want).any(0).nonzero().flatten().tolist()
+        assert not bad, f"{off}: {len(bad)} of {H} columns: {[(float(m[i]), float(got[0, i])) for i in bad[:4]]}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,H,shift,size", [(1, 128, 0, 0.75), (3, 512, 0, 0.75), (1030, 256, 0, 0.75),
+                                            (1027, 1024, 0, 0.75), (2, 20480, 0, 0.75), (2, 256, -126, 0.375),
+                                            (1, 4096, 121, 12.0), (1025, 4096, 121, 12.0)])
+def test_e4m3(T, H, shift, size, dtype):
+    """5-bit odd numbers in every binade, half way between two of 4 bits, and odd multiples of
+    half the smallest step; a largest value of 256 in each block makes its scale 1. The same at
+    the smallest scale, and past the range of fp32 (there one block, the others zeros)."""
+    cases, steps = [256.0], {256.0: 0.0}
+    for j in range(-10, 5):
+        for y in range(17 if j > -10 else 1, 32 if j < 4 else 28, 2):
+            cases.append(y * 2.0 ** j)
+            steps[cases[-1]] = 2.0 ** j
+    cases.append(256.0)  # 128: a block each sign
+    assert len(cases) == 128
+    unit = 2.0 ** shift
+    cases = [(y * unit, size, y * unit * 3 / size) for y in cases]
+    if shift > 0:
+        cases += [(0.0, 0.0, 0.0)] * (H - 128)
+    t, w, m = row(cases, H, dtype)
+    step = torch.tensor([steps.get(v, 0.0) for v in (m.abs() / unit).tolist()], dtype=torch.float64) * unit
+    for off in OFFS:
+        q, scale = norm(t, w, off, T, dtype, q_dtype=torch.float8_e4m3fn)[2:]
+        assert (scale[:, 0] == unit).all() and ((scale == unit) | (scale == 1)).all()
+        want = m + m.sign() * (step if off > 0 else -step)
+        got = q.double().cpu() * scale.double().cpu().repeat_interleave(128, 1)
         bad = (got != want).any(0).nonzero().flatten().tolist()
         assert not bad, f"{off}: {len(bad)} of {H} columns: {[(float(m[i]), float(got[0, i])) for i in bad[:4]]}"
