@@ -231,6 +231,25 @@ hipError_t launch_dispatch_fp8(const void* x, int dtype, const int32_t* pos, int
 hipError_t launch_gemm_fp8(const void* a, const float* asc, int64_t rows, int E,
                            const int32_t* offs, const int32_t* cnts, const void* w,
                            const float* wsc, int N, int K, void* out, hipStream_t s);
+// Rows an expert, on average, up to which a product streams the weights: the tiled kernel, which
+// reads a weight once for all rows, gains with fewer steps a tile. 128 experts, even routing,
+// streamed against tiled (us):
+//   K     N 2816                                  N 4096
+//   1408  14 rows 95, 98;   18 rows 102, 98       14 rows 135, 134;  18 rows 145, 135
+//   2816  16 rows 180, 184; 18 rows 186, 185      14 rows 251, 255;  16 rows 258, 253
+//   3584  22 rows 230, 234; 28 rows 237, 235      22 rows 324, 325;  24 rows 330, 326
+//   3840  20 rows 247, 248; 24 rows 253, 249
+//   4096  28 rows 274, 303; 32 rows 266, 307      26 rows 368, 368;  30 rows 374, 367
+//   5632  26 rows 362, 363; 30 rows 368, 365
+//   7168  26 rows 456, 458; 30 rows 467, 458      24 rows 630, 633;  28 rows 650, 636
+// So 14 rows up to K 2816, 28 from 4096 on, between them by the line (1.5% lost at K 3968, 24
+// rows; 14 up to there lost 4% at K 3584, 16 rows). Rows of weights that are no
+// whole lines gain earlier, their lines being cut at every step (100 experts: K 4112, N 2816: 6
+// rows 237 and 240, 10 rows 250 and 243; K 1392, N 4096: 6 rows 122 and 126, 10 rows 130 and 127).
+inline int64_t gemm_int8_stream_rows(int64_t K) {
+  if (K % 128) return 8;
+  return K <= 2816 ? 14 : (K >= 4096 ? 28 : 14 + (K - 2816) * 14 / 1280);
+}
 // Whether that product (or the gate/up product) streams the weights, in tiles of
 // kStreamRows rows by kStreamCols of the N rows of w. Rows an expert on average up to
 // which that is the faster: 128 experts, N 2816, K 4096, even routing: 16 rows 258 against
@@ -287,16 +306,10 @@ hipError_t launch_gemm_int8(const Int8Rows& a, int64_t rows, int E, const int32_
 // rows an expert on average, bound by the weights' bytes either way; or few results in all,
 // where the tiled kernel is bound by the latency of its K steps, 19 us for K 4096 however few
 // they are (N 4096, one expert: 64 rows 9.6 against 19 us, 128 rows 12, 256 rows 17, 384
-// rows 26). The tiled kernel gains with fewer steps a tile, since it reads a weight once for
-// all rows: 128 experts, even routing, streamed against tiled: K 4096, N 2816: 16 rows 252 and
-// 278 us, 28 rows 290 and 290; K 1408, N 4096: 8 rows 122 and 131, 12 rows 134 and 134, 28
-// rows 158 and 139; K 2816: 16 rows 262 and 256. Rows of weights that are no whole lines gain
-// earlier, their lines being cut at every step (100 experts: K 4112, N 2816: 6 rows 237 and
-// 240, 10 rows 250 and 243, 22 rows 294 and 251; K 1392, N 4096: 6 rows 122 and 126, 10 rows
-// 130 and 127). One K step is too short for its stream of loads.
+// rows 26).
 inline bool gemm_int8_streams(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int64_t padded = rows + 16 * (rows < E ? rows : E);  // the tiles' rows, on average
-  return K <= 128 || rows <= (K % 128 ? 8 : K < 4096 ? 14 : 28) * E ||
+  return K <= 128 || rows <= gemm_int8_stream_rows(K) * E ||
          padded * N <= (int64_t(1) << 20) + 16 * N;
 }
 // The waves that share one group of weight rows in the streamed kernel, each a part of K
