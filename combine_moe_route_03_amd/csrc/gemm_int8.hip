@@ -500,10 +500,16 @@ hipError_t gemm(Out out, const Int8Rows& a, int64_t rows, int E, const int32_t* 
   if (gemm_int8_streams(rows, E, N, K))
     return launch_gemm_int8_stream(out == Out::kGateUp, out != Out::kBF16, a, rows, E, offs, cnts, w,
                                    wsc, N, K, c, s);
-  // tiles of 256 rows, on average half a one more an expert; the stream of loads is at
-  // least as many steps long as there are stages
-  const int64_t tiles = (rows / 256 + (rows < E ? rows : E)) * ((N + 255) / 256);
-  const bool small = K > 256 && (rows <= (int64_t)128 * E || tiles <= 160);
+  // Tiles of 128 rows where they are one round of the units at most (half a tile more an expert
+  // on average), or the experts have no more rows than that; the stream of loads is at least as
+  // many steps long as there are stages. 128 against 256 rows a tile (us), even routing:
+  //   N, K 4096, one expert: 1992 rows, 256 tiles 31.8, 36.1; 2504 rows, 320 tiles 47.0, 42.3
+  //   N 4096, K 1024: 13.4, 14.6; 18.1, 17.3        K 7168: 53.8, 68.7; 78.4, 69.2
+  //   N 4096, K 7168, 8 experts of 160 rows, 256 tiles 49.4, 60.7; of 288 rows 84.6, 81.2
+  //   N 2816, K 4096, 64 experts of 128 rows 168, 183; of 160 196, 200; of 224 217, 210
+  //   N 2048, K 1408, 64 experts of 128 rows 36.6, 41.4; of 160 45.4, 43.9; of 224 50.3, 48.2
+  const int64_t tiles = (rows + 64 * (rows < E ? rows : E)) / 128 * ((N + 255) / 256);
+  const bool small = K > 256 && (rows <= (int64_t)128 * E || tiles <= kUnitsPerXcd * kXCD);
   const auto of = [&](auto o) {
     constexpr Out O = decltype(o)::value;
     if (small)

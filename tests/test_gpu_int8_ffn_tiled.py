@@ -16,8 +16,8 @@ def rows_of_a_tile(rows, E, N, K):
     """Rows of a tile of the kernel that a product takes; 0: streamed."""
     if not tiled(rows, E, N, K):
         return 0
-    tiles = (rows // 256 + min(rows, E)) * ((N + 255) // 256)
-    return 128 if K > 256 and (rows <= 128 * E or tiles <= 160) else 256
+    tiles = (rows + 64 * min(rows, E)) // 128 * ((N + 255) // 256)
+    return 128 if K > 256 and (rows <= 128 * E or tiles <= 256) else 256
 
 
 def uneven(E, rows, seed):

@@ -31,3 +31,24 @@ def test_streamed_or_tiled_by_k(K):
         assert total == rows
         print(f"[rule] K={K} rows={rows}", flush=True)
         check(ints(rows, K, seed=1), scales(rows, seed=2), offs, cnts, w, sw)
+
+
+def one_round(rows, E, N):
+    """Whether tiles of 128 rows by 256 columns are a round of the units, as the library has it."""
+    return (rows + 64 * min(rows, E)) // 128 * ((N + 255) // 256) <= 256
+
+
+@pytest.mark.parametrize("E,N,K,rows", [(1, 4112, 400, 1983), (1, 4112, 400, 1984), (1, 2048, 1024, 4159),
+                                        (1, 2048, 1024, 4160), (7, 4096, 784, 1727), (7, 4096, 784, 1728),
+                                        (12, 2816, 528, 2303), (12, 2816, 528, 2304)])
+def test_tiles_of_128_or_256_rows(E, N, K, rows):
+    assert rows > 128 * E and (rows + 16 * E) * N > 2 ** 20 + 16 * N
+    assert one_round(rows, E, N) == (rows % 2 == 1) and one_round(rows - 1, E, N)
+    counts = [rows // E] * E
+    counts[0] += rows - sum(counts)
+    if E > 3:
+        counts[1], counts[2] = counts[1] + 129, counts[2] - 129
+    offs, cnts, total = buckets(counts)
+    assert total == rows
+    print(f"[rule] E={E} N={N} K={K} rows={rows}", flush=True)
+    check(ints(rows, K, seed=1), scales(rows, seed=2), offs, cnts, ints(E, N, K, seed=3), scales(E, N, seed=4))
