@@ -127,7 +127,7 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* lds
 }
 
 // m-tile prefix sums of the experts in LDS: pre[e] m-tiles before expert e, pre[E] in
-// all (gemm_fp8.h says which buckets count). Called by the whole block.
+// all (bucket_tiles says which buckets count). Called by the whole block.
 template <int BM>
 __device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ offs,
                                             const int32_t* __restrict__ cnts, int E,

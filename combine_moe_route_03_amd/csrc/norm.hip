@@ -10,8 +10,10 @@
 //
 // Bound by HBM bytes: every element is read once and kept in registers between the
 // row's reduction and the outputs. Norm of 16384 x 7168 bf16 with the residual, y and int8 rows
-// out: 172 us, 6.1 TB/s; 45056 x 4096 bf16 to int8: 86 us, 6.4 TB/s. One row of 4096: 3.4 us
-// in a graph, latency.
+// out: 173-176 us, 6.0-6.1 TB/s; 45056 x 4096 bf16 to int8: 86 us, 6.4 TB/s. One row of 4096:
+// 3.7 us in a graph, latency. Norms of rows wider than 32768 do not fit the 128 registers of a
+// block of 1024 threads and keep part of a row in scratch memory (512 rows of 65536, int8 rows
+// out: bf16 78 us, 3.9 TB/s; fp32 229 us, 2.5 TB/s).
 #include <type_traits>
 
 #include "device.h"

@@ -435,7 +435,7 @@ int moe_add_rms_norm(int32_t dtype, int32_t q_dtype, int32_t T, int32_t H, const
  *   out[n][c] = round( S a_scale[r] w_scale[e][c] ),  S = sum_j a[r][j] w[e][c][j]
  * for every row n in [expert_offsets[e], + expert_counts[e]); other rows are untouched.
  * r = n, or row_token[n] where row_token is given: the rows are then picked from a_rows
- * tokens and need no dispatch copy (an index outside [0, a_rows) gives a row of zeros). S is
+ * tokens and need no dispatch copy (an index outside [0, a_rows) is a row of zeros with scale 0). S is
  * exact; it and its products with the two scales, in that order, are rounded to fp32,
  * the last one once more to out_dtype (MOE_BF16 or MOE_F32). A dense product is E = 1 with offsets {0}
  * and counts {rows}. Buckets may lie in any order and do not overlap; one that does not lie
